@@ -72,6 +72,8 @@ typedef enum wm_status {
 #define WM_DEVERR_BAD_PAGE 2     /* block-table entry outside [0, n_pages) */
 #define WM_DEVERR_TIMEOUT 3      /* a pipeline wait exceeded its iteration limit */
 #define WM_DEVERR_INTERNAL 4     /* a kernel's own address-range self-check failed (the access was skipped) */
+#define WM_DEVERR_BAD_TOKEN 5    /* a drafted token outside [0, vocab) (it is refused) */
+#define WM_DEVERR_BAD_PROB 6     /* a row of target probabilities without any weight (token -1 is returned) */
 
 /*
  * The draft's compact ring buffer (one per draft attention layer).
@@ -365,6 +367,140 @@ int32_t wm_verify_persistent(int32_t batch, int32_t n_kv_heads, int32_t n_q_head
  */
 size_t wm_workspace_size(int32_t op, int32_t batch, int32_t n_kv_heads, int32_t n_q_heads,
                          int32_t n_q, int32_t head_dim, int64_t max_keys, int32_t n_split);
+
+/*
+ * A full-context KV cache held in 4 bits, contiguous or paged: the target's
+ * cache in about a quarter of the bf16 bytes.
+ *
+ * Per position and KV head, K and V each have a scale s and a zero z (bf16)
+ * and one 4-bit code c per channel; the value held is s c + z.  64 positions of
+ * one KV head form a record of 64 head_dim + 512 bytes
+ * (wm_kvq_record_bytes):
+ *   K codes  [head_dim / 32][64][16]  byte-units: 32 channels of one position
+ *   V codes  [2][head_dim][16]        byte-units: 32 positions of one channel
+ *   K (s, z) [64][2] bf16
+ *   V (s, z) [64][2] bf16
+ * In a little-endian 32-bit word, element e of its 8 is at bits
+ * 4 * (e / 2 + 4 * (e % 2)).
+ *   contiguous (block_table == NULL):
+ *       data  [batch][n_kv_heads][n_cap / 64][record]; n_cap a multiple of 64
+ *   paged (block_table != NULL):
+ *       data  [n_pages][n_kv_heads][page_size / 64][record]; page_size a
+ *       multiple of 64; block_table [batch][max_pages] int32 as for wm_kv
+ *   seq_lens [batch] int64: number of valid positions of each sequence.
+ * data must be 16-byte aligned.  No initial contents are needed: positions at or
+ * past seq_lens[b] are never used, whatever their bytes.  A page that an append
+ * writes must belong to one sequence.
+ */
+typedef struct wm_kvq {
+    void *data;
+    const int64_t *seq_lens;
+    const int32_t *block_table;
+    int64_t n_cap;   /* contiguous: positions per (sequence, head) row */
+    int64_t n_pages; /* paged: pages in the pool */
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t batch;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+} wm_kvq;
+
+/* Bytes of one record, 0 if head_dim is not 64, 128 or 256. */
+size_t wm_kvq_record_bytes(int32_t head_dim);
+
+/*
+ * Quantise n_new new positions of every sequence into the cache.  As for
+ * wm_verify_attn the new positions are the last ones: token i of sequence b is
+ * written at position seq_lens[b] - n_new + i (set seq_lens to the new
+ * lengths first; layers that share them append one after the other).  Tokens
+ * whose position would be negative are padding and are skipped.
+ *   k_new, v_new  [batch][n_new][n_kv_heads][head_dim] bf16, 16-byte aligned.
+ * Per token, head and K or V, over the channels x_d, with the arithmetic of
+ * real numbers (the result is the same bits on every call):
+ *   z = min x_d;  s = bf16((max x_d - z) / 15), to nearest even;
+ *   c_d = min(15, max(0, rint((x_d - z) / s))), ties to even;  c_d = 0 if s = 0.
+ * (Differences and quotients as doubles give them.)  A row that holds a NaN or an infinity
+ * gets s = z = NaN and attention over it gives NaN.  Other positions of the
+ * records keep their codes.  A seq_lens[b] that is negative or beyond the capacity records
+ * WM_DEVERR_BAD_LENGTH and nothing is written for b; a block-table entry
+ * outside the pool records WM_DEVERR_BAD_PAGE and its positions are skipped.
+ */
+wm_status wm_kvq_append(const wm_kvq *kv, const void *k_new, const void *v_new, int32_t n_new, void *stream);
+
+/*
+ * Read the last n positions back: row i of sequence b is position
+ * seq_lens[b] - n + i, each value s c + z rounded to bf16 (for a bf16 copy of
+ * a sequence's tail, e.g. the history of wm_ring_fill).  Rows before position 0, and rows in a
+ * page outside the pool (WM_DEVERR_BAD_PAGE), are 0; a length beyond the capacity
+ * records WM_DEVERR_BAD_LENGTH and is clamped.
+ *   k_out, v_out  [batch][n][n_kv_heads][head_dim] bf16, 16-byte aligned.
+ */
+wm_status wm_kvq_read(const wm_kvq *kv, int32_t n, void *k_out, void *v_out, void *stream);
+
+/*
+ * wm_verify_attn over a 4-bit cache: query i (0 <= i < n_q) of sequence b sits at
+ * position seq_lens[b] - n_q + i and attends causally to keys 0 .. that
+ * position, with the values the cache holds.  n_q = 1 is single-token decode.
+ *   q, out  [batch][n_q][n_q_heads][head_dim] bf16;  lse [batch][n_q][n_q_heads]
+ *           fp32 or NULL;  16-byte (q, out) and 4-byte (lse) aligned.
+ *   workspace  wm_kvq_workspace_size(...) bytes, 256-byte aligned; no initial
+ *              contents.  Calls that can overlap on the GPU need one each.
+ * The work is split on the device from the actual lengths: one CTA per SM takes
+ * an equal run of the batch's 128-position tiles.  Two launches.  Results do
+ * not depend on what else runs: repeated calls are bit-identical.
+ * At most 64 rows (n_q * n_q_heads / n_kv_heads) per KV head and 2^30 tiles
+ * (batch * n_kv_heads * ceil(capacity / 128)); WM_ERR_UNSUPPORTED beyond.
+ */
+wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32_t n_q_heads, float scale, void *out,
+                             float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Workspace bytes of wm_verify_attn_kvq on the current device; never 0.
+ * Returns (size_t)-1 on invalid arguments.
+ */
+size_t wm_kvq_workspace_size(int32_t batch, int32_t n_kv_heads, int32_t n_q_heads, int32_t n_q, int32_t head_dim);
+
+/*
+ * Verification of drafted tokens by speculative sampling, from given random
+ * numbers.  Per sequence b, with n = n_draft[b] drafts x_0 .. x_{n-1}:
+ *   draft j is accepted while  u_accept[b][j] * q_j(x_j) < p_j(x_j); the first
+ *   that fails ends it, a = the accepted count;
+ *   one more token is drawn by inversion with w = u_sample[b] from
+ *       r = max(p_a - q_a, 0)  if a < n,    r = p_n  if all were accepted:
+ *   the least i with r_0 + .. + r_i > w (r_0 + .. + r_{vocab-1}) (the last i
+ *   with r_i > 0 if rounding leaves none).  If the first r has no weight at
+ *   all, r = p_a.
+ * This keeps the target's distribution if the drafts were drawn from q and the
+ * u's are uniform in [0, 1) and independent.
+ *   target_probs  [batch][k + 1][vocab] fp32, row j the target's distribution of
+ *                 the token after position j of the verified tokens
+ *   draft_probs   [batch][k][vocab] fp32, or NULL for drafts without
+ *                 probabilities (n-gram, retrieval, greedy): q_j is then 1 at
+ *                 x_j and 0 elsewhere
+ *   draft_tokens  [batch][k] int32
+ *   n_draft       [batch] int32, 0 <= n_draft[b] <= k, or NULL for k.  Drafts past it
+ *                 are not read (nor are the rows of probabilities)
+ *   u_accept      [batch][k] fp32;  u_sample [batch] fp32
+ *   seq_lens      [batch] int64 or NULL: cache length with the k + 1 verified
+ *                 positions (the last sampled token and the k drafts)
+ *   tokens        out [batch][k + 1] int32: the accepted drafts, the drawn token, then -1
+ *   n_accepted    out [batch] int32: a
+ *   new_len       out [batch] int64 or NULL (needs seq_lens; may be the same
+ *                 array): seq_lens[b] - k + a, the positions that stay valid --
+ *                 what wm_ring_rollback takes
+ * Greedy verification: pass one-hot target rows.  Probabilities need not sum
+ * to 1; a NaN or negative one counts as 0, one above 1 as 1, and the same holds for the u's.
+ * The sums carry about 48 bits, in an order that the shapes alone fix.
+ * n_draft[b] outside [0, k] records WM_DEVERR_BAD_LENGTH and is clamped; a
+ * draft outside [0, vocab) records WM_DEVERR_BAD_TOKEN and is refused; a
+ * row without weight records WM_DEVERR_BAD_PROB and gives token -1.
+ * k >= 1, batch <= 65535.  One launch, no workspace.  The outputs must not
+ * overlap the inputs otherwise.
+ */
+wm_status wm_spec_accept(const float *target_probs, const float *draft_probs, const int32_t *draft_tokens,
+                         const int32_t *n_draft, const float *u_accept, const float *u_sample,
+                         const int64_t *seq_lens, int32_t batch, int32_t k, int32_t vocab, int32_t *tokens,
+                         int32_t *n_accepted, int64_t *new_len, void *stream);
 
 /*
  * Synchronise `stream`, then read and clear the device error word of the

@@ -8,6 +8,7 @@
 #include <functional>
 #include <mutex>
 
+#include "kvq.cuh"
 #include "wm_internal.h"
 #include "../../include/wm_api.h"
 
@@ -357,6 +358,61 @@ bool mem_ok(const wm_mem *m) {
 // 64-key tiles, so that every tile is all ring or all memory.
 int64_t mem_base_of(const wm_ring *ring) {
     return ((int64_t)ring->sink + ring->window + kKeyTile - 1) / kKeyTile * kKeyTile;
+}
+
+// ---- 4-bit cache
+
+wm_status kvq_check(const wm_kvq *kv) {
+    if (!kv || !kv->data || !kv->seq_lens || kv->batch <= 0 || kv->n_kv_heads <= 0) return WM_ERR_INVALID_ARG;
+    if (!head_dim_ok(kv->head_dim)) return WM_ERR_UNSUPPORTED;
+    if (!aligned(kv->data, 16) || !aligned(kv->seq_lens, 8)) return WM_ERR_INVALID_ARG;
+    if (kv->block_table) {
+        if (kv->page_size <= 0 || kv->max_pages <= 0 || kv->n_pages <= 0 || !aligned(kv->block_table, 4))
+            return WM_ERR_INVALID_ARG;
+        if (kv->page_size % kRecKeys || kv->n_pages > INT32_MAX ||
+            (int64_t)kv->max_pages * kv->page_size > INT32_MAX)
+            return WM_ERR_UNSUPPORTED;
+    } else {
+        if (kv->n_cap <= 0) return WM_ERR_INVALID_ARG;
+        if (kv->n_cap % kRecKeys || kv->n_cap > INT32_MAX) return WM_ERR_UNSUPPORTED;
+    }
+    if ((int64_t)kv->batch * kv->n_kv_heads > kMaxUnits) return WM_ERR_UNSUPPORTED;
+    return WM_OK;
+}
+
+KvqView kvq_view(const wm_kvq *kv) {
+    KvqView c = {};
+    c.data = static_cast<uint8_t *>(kv->data);
+    c.seq_lens = kv->seq_lens;
+    c.block_table = kv->block_table;
+    c.capacity = kv->block_table ? (int64_t)kv->max_pages * kv->page_size : kv->n_cap;
+    c.n_pages = kv->block_table ? kv->n_pages : kv->batch;
+    c.recs_per_page = (int32_t)((kv->block_table ? kv->page_size : kv->n_cap) / kRecKeys);
+    c.max_pages = kv->max_pages;
+    c.batch = kv->batch;
+    c.n_kv_heads = kv->n_kv_heads;
+    c.head_dim = kv->head_dim;
+    return c;
+}
+
+// Workspace of the attention over a 4-bit cache: parts, their log-sum-exps and
+// the schedule, each 256-byte aligned.
+struct KvqLayout {
+    size_t lse = 0, sched = 0, total = 0;
+};
+KvqLayout kvq_layout(int n_cta, int64_t units, int rows, int head_dim, int batch) {
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t n_part = (size_t)n_cta + (size_t)units - 1;
+    KvqLayout l;
+    l.lse = up(n_part * rows * head_dim * sizeof(float));
+    l.sched = l.lse + up(n_part * rows * sizeof(float));
+    l.total = l.sched + ((size_t)batch + 2) * sizeof(int64_t);
+    return l;
+}
+// One CTA per SM.
+int kvq_ctas() {
+    const int sms = sm_count();
+    return sms > 0 ? sms : 1;
 }
 
 }  // namespace
@@ -762,6 +818,107 @@ wm_status wm_verify_attn(const wm_kv *kv, const void *q, int32_t n_q, int32_t n_
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     return run_attention(WM_OP_VERIFY, p, maps, capacity, n_split, out, lse, workspace, workspace_bytes,
                          static_cast<cudaStream_t>(stream));
+}
+
+size_t wm_kvq_record_bytes(int32_t head_dim) { return head_dim_ok(head_dim) ? (size_t)rec_bytes(head_dim) : 0; }
+
+wm_status wm_kvq_append(const wm_kvq *kv, const void *k_new, const void *v_new, int32_t n_new, void *stream) {
+    const wm_status ks = kvq_check(kv);
+    if (ks != WM_OK) return ks;
+    if (!k_new || !v_new || n_new <= 0 || !aligned(k_new, 16) || !aligned(v_new, 16)) return WM_ERR_INVALID_ARG;
+    int32_t *err = device_error_ptr();
+    if (!err) return WM_ERR_CUDA;
+    return launch_status(
+        launch_kvq_append(kvq_view(kv), k_new, v_new, n_new, err, static_cast<cudaStream_t>(stream)));
+}
+
+wm_status wm_kvq_read(const wm_kvq *kv, int32_t n, void *k_out, void *v_out, void *stream) {
+    const wm_status ks = kvq_check(kv);
+    if (ks != WM_OK) return ks;
+    if (!k_out || !v_out || n <= 0 || !aligned(k_out, 16) || !aligned(v_out, 16)) return WM_ERR_INVALID_ARG;
+    int32_t *err = device_error_ptr();
+    if (!err) return WM_ERR_CUDA;
+    return launch_status(launch_kvq_read(kvq_view(kv), n, k_out, v_out, err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t wm_kvq_workspace_size(int32_t batch, int32_t n_kv_heads, int32_t n_q_heads, int32_t n_q, int32_t head_dim) {
+    if (batch <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q <= 0 || n_q_heads % n_kv_heads || !head_dim_ok(head_dim) ||
+        (int64_t)batch * n_kv_heads > kMaxUnits || (int64_t)n_q * (n_q_heads / n_kv_heads) > kMaxRows)
+        return (size_t)-1;
+    return kvq_layout(kvq_ctas(), (int64_t)batch * n_kv_heads, n_q * (n_q_heads / n_kv_heads), head_dim, batch).total;
+}
+
+wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32_t n_q_heads, float scale, void *out,
+                             float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    const wm_status ks = kvq_check(kv);
+    if (ks != WM_OK) return ks;
+    if (!q || !out || n_q <= 0 || n_q_heads <= 0 || !std::isfinite(scale)) return WM_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return WM_ERR_INVALID_ARG;
+    if (n_q_heads % kv->n_kv_heads) return WM_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)(n_q_heads / kv->n_kv_heads) * n_q;
+    if (rows > kMaxRows) return WM_ERR_UNSUPPORTED;
+    KvqAttnParams p;
+    std::memset(&p, 0, sizeof p);
+    p.c = kvq_view(kv);
+    const int64_t units = (int64_t)kv->batch * kv->n_kv_heads;
+    // tile counts stay within 32 bits
+    if (units * ((p.c.capacity + kKvqTile - 1) / kKvqTile) > (int64_t)1 << 30) return WM_ERR_UNSUPPORTED;
+    const int n_cta = kvq_ctas();
+    const KvqLayout l = kvq_layout(n_cta, units, (int)rows, kv->head_dim, kv->batch);
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return WM_ERR_WORKSPACE;
+    char *w = static_cast<char *>(workspace);
+    p.q = q;
+    p.n_q = n_q;
+    p.n_q_heads = n_q_heads;
+    p.group = n_q_heads / kv->n_kv_heads;
+    p.rows = (int)rows;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.o_part = reinterpret_cast<float *>(w);
+    p.lse_part = reinterpret_cast<float *>(w + l.lse);
+    p.sched = reinterpret_cast<int64_t *>(w + l.sched);
+    p.out = out;
+    p.lse = lse;
+    p.err = device_error_ptr();
+    if (!p.err) return WM_ERR_CUDA;
+    p.wait_limit = t_wait_limit;
+    p.stall_tile = t_stall_tile;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_kvq_attn(p, n_cta, st);
+    if (e != cudaSuccess) return WM_ERR_CUDA;
+    return launch_status(launch_kvq_merge(p, st));
+}
+
+wm_status wm_spec_accept(const float *target_probs, const float *draft_probs, const int32_t *draft_tokens,
+                         const int32_t *n_draft, const float *u_accept, const float *u_sample,
+                         const int64_t *seq_lens, int32_t batch, int32_t k, int32_t vocab, int32_t *tokens,
+                         int32_t *n_accepted, int64_t *new_len, void *stream) {
+    if (!target_probs || !draft_tokens || !u_accept || !u_sample || !tokens || !n_accepted || batch <= 0 || k <= 0 ||
+        vocab <= 0 || (new_len && !seq_lens))
+        return WM_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)target_probs, (const void *)draft_probs, (const void *)draft_tokens,
+                          (const void *)n_draft, (const void *)u_accept, (const void *)u_sample, (const void *)tokens,
+                          (const void *)n_accepted})
+        if (!aligned(x, 4)) return WM_ERR_INVALID_ARG;
+    if (!aligned(seq_lens, 8) || !aligned(new_len, 8)) return WM_ERR_INVALID_ARG;
+    // entry indexes within a row, rounded up to whole runs, stay within 32 bits
+    if (batch > kMaxUnits || vocab > (1 << 30) || k > (1 << 20)) return WM_ERR_UNSUPPORTED;
+    AcceptParams p;
+    p.target_probs = target_probs;
+    p.draft_probs = draft_probs;
+    p.draft_tokens = draft_tokens;
+    p.n_draft = n_draft;
+    p.u_accept = u_accept;
+    p.u_sample = u_sample;
+    p.seq_lens = seq_lens;
+    p.tokens = tokens;
+    p.n_accepted = n_accepted;
+    p.new_len = new_len;
+    p.batch = batch;
+    p.k = k;
+    p.vocab = vocab;
+    p.err = device_error_ptr();
+    if (!p.err) return WM_ERR_CUDA;
+    return launch_status(launch_spec_accept(p, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

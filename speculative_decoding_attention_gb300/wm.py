@@ -19,12 +19,14 @@ from . import build as _build
 WM_OK, WM_ERR_INVALID_ARG, WM_ERR_UNSUPPORTED, WM_ERR_WORKSPACE, WM_ERR_CUDA, WM_ERR_DEVICE_DATA = range(6)
 WM_OP_DRAFT, WM_OP_VERIFY, WM_OP_DRAFT_STEP, WM_OP_DRAFT_MEM = 0, 1, 2, 3
 WM_DRAFT_MATH_MMA, WM_DRAFT_MATH_FMA = 0, 1
-DEVERR_NAMES = {0: "none", 1: "bad length", 2: "bad page", 3: "pipeline wait timeout", 4: "internal check"}
+DEVERR_NAMES = {0: "none", 1: "bad length", 2: "bad page", 3: "pipeline wait timeout", 4: "internal check",
+                5: "bad token", 6: "row without weight"}
 
 EXPORTED = ("wm_ring_append", "wm_ring_fill", "wm_ring_rollback", "wm_draft_attn", "wm_verify_attn",
             "wm_lse_merge", "wm_plan_splits", "wm_verify_persistent", "wm_workspace_size", "wm_get_device_error",
             "wm_status_string", "wm_version", "wm_draft_attn_static", "wm_draft_step", "wm_draft_attn_mem",
-            "wm_mem_append", "wm_mem_rollback", "wm_set_test_stall", "wm_set_draft_math")
+            "wm_mem_append", "wm_mem_rollback", "wm_set_test_stall", "wm_set_draft_math", "wm_kvq_record_bytes",
+            "wm_kvq_append", "wm_kvq_read", "wm_verify_attn_kvq", "wm_kvq_workspace_size", "wm_spec_accept")
 STATIC_SCRATCH_BYTES = 8 << 20  # WM_STATIC_SCRATCH_BYTES
 
 _lib = None
@@ -54,6 +56,13 @@ class _KV(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("n_cap", ctypes.c_int64), ("n_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KVQ(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("n_cap", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -99,6 +108,16 @@ def load() -> ctypes.CDLL:
         lib.wm_set_test_stall.restype = I32
         lib.wm_set_draft_math.argtypes = [I32]
         lib.wm_set_draft_math.restype = I32
+        lib.wm_kvq_record_bytes.argtypes = [I32]
+        lib.wm_kvq_record_bytes.restype = ctypes.c_size_t
+        lib.wm_kvq_append.argtypes = [P, P, P, I32, P]
+        lib.wm_kvq_read.argtypes = [P, I32, P, P, P]
+        lib.wm_verify_attn_kvq.argtypes = [P, P, I32, I32, F, P, P, P, ctypes.c_size_t, P]
+        lib.wm_kvq_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+        lib.wm_kvq_workspace_size.restype = ctypes.c_size_t
+        lib.wm_spec_accept.argtypes = [P, P, P, P, P, P, P, I32, I32, I32, P, P, P, P]
+        for name in ("wm_kvq_append", "wm_kvq_read", "wm_verify_attn_kvq", "wm_spec_accept"):
+            getattr(lib, name).restype = I32
         for name in ("wm_ring_append", "wm_ring_fill", "wm_ring_rollback", "wm_draft_attn", "wm_draft_attn_static",
                      "wm_verify_attn", "wm_lse_merge", "wm_get_device_error"):
             getattr(lib, name).restype = I32
@@ -460,6 +479,203 @@ def lse_merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out=None, lse=None
                                n_parts, rows, D, _dev(out, torch.bfloat16, "out"),
                                _dev(lse, torch.float32, "lse"), _stream(stream)), "wm_lse_merge")
     return out, lse
+
+
+def _arg(t: torch.Tensor, dtype, shape: tuple, device: int, what: str) -> int:
+    """Address of an argument of the given type and shape on the current device."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on the current device (cuda:{device}), is on {t.device}")
+    return t.data_ptr()
+
+
+def _new_on(stream, shape: tuple, dtype, device: int) -> torch.Tensor:
+    """A buffer that belongs to the stream the call runs on, so that its memory
+    is handed on in that stream's order."""
+    if stream is None:
+        return _new_out(shape, dtype, device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return _new_out(shape, dtype, device)
+
+
+def _new_int(stream, shape: tuple, dtype, device: int) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+KVQ_RECORD_KEYS = 64  # positions per record
+
+
+def kvq_record_bytes(head_dim: int) -> int:
+    """Bytes of one 64-position record of one KV head (see wm_kvq in include/wm_api.h)."""
+    n = int(load().wm_kvq_record_bytes(head_dim))
+    if n == 0:
+        raise ValueError(f"head_dim must be 64, 128 or 256, got {head_dim}")
+    return n
+
+
+class KVQCache:
+    """A KV cache held in 4 bits (``wm_kvq``): ``data`` uint8, contiguous
+    [B, Hkv, n_cap / 64, record] or paged [n_pages, Hkv, page_size / 64, record]
+    with a block table [B, max_pages] int32; ``seq_lens`` [B] int64.  The handle
+    keeps the tensors; their contents may change, they may not be replaced."""
+
+    __slots__ = ("data", "seq_lens", "block_table", "batch", "n_kv_heads", "head_dim", "capacity", "device", "_c",
+                 "_ref")
+
+    def __init__(self, data: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor | None = None):
+        if data.dim() != 4 or data.shape[3] not in (64 * 64 + 512, 64 * 128 + 512, 64 * 256 + 512):
+            raise ValueError(f"data must be [*, Hkv, positions / 64, 64 * head_dim + 512], got {tuple(data.shape)}")
+        if seq_lens.dim() != 1 or (block_table is not None and (block_table.dim() != 2 or
+                                                                block_table.shape[0] != seq_lens.shape[0])):
+            raise ValueError("seq_lens must be [B] and block_table [B, max_pages]")
+        if block_table is None and data.shape[0] != seq_lens.shape[0]:
+            raise ValueError("a contiguous cache holds one row of records per sequence and head")
+        device = data.get_device()
+        c = _KVQ()
+        c.data = _arg(data, torch.uint8, data.shape, device, "kvq.data")
+        c.seq_lens = _arg(seq_lens, torch.int64, seq_lens.shape, device, "kvq.seq_lens")
+        c.batch, c.n_kv_heads, c.head_dim = seq_lens.shape[0], data.shape[1], (data.shape[3] - 512) // 64
+        inner = data.shape[2] * KVQ_RECORD_KEYS
+        if block_table is not None:
+            c.block_table = _arg(block_table, torch.int32, block_table.shape, device, "kvq.block_table")
+            c.n_pages, c.page_size, c.max_pages = data.shape[0], inner, block_table.shape[1]
+            self.capacity = inner * block_table.shape[1]
+        else:
+            c.n_cap = inner
+            self.capacity = inner
+        self.data, self.seq_lens, self.block_table = data, seq_lens, block_table
+        self.batch, self.n_kv_heads, self.head_dim, self.device = c.batch, c.n_kv_heads, c.head_dim, device
+        self._c, self._ref = c, ctypes.byref(c)
+
+    @classmethod
+    def create(cls, batch: int, n_kv_heads: int, head_dim: int, capacity: int, device="cuda") -> "KVQCache":
+        """An empty contiguous cache for ``capacity`` positions per sequence (rounded up to whole records)."""
+        blocks = -(-capacity // KVQ_RECORD_KEYS)
+        data = torch.zeros((batch, n_kv_heads, blocks, kvq_record_bytes(head_dim)), dtype=torch.uint8, device=device)
+        return cls(data, torch.zeros((batch,), dtype=torch.int64, device=device))
+
+    @property
+    def paged(self) -> bool:
+        return self.block_table is not None
+
+
+def _kvq_device(cache: KVQCache) -> int:
+    device = torch.cuda.current_device()
+    if cache.device != device:
+        raise ValueError(f"the cache must be on the current device (cuda:{device}), is on cuda:{cache.device}")
+    return device
+
+
+def kvq_append(cache: KVQCache, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+    """Quantise new tokens k_new, v_new [B, n, Hkv, D] bf16 into the cache at the
+    last n positions (seq_lens already holds the new lengths)."""
+    device = _kvq_device(cache)
+    if k_new.dim() != 4:
+        raise ValueError(f"k_new must be [B, n, Hkv, D], got {tuple(k_new.shape)}")
+    n = k_new.shape[1]
+    shape = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
+    _check(load().wm_kvq_append(cache._ref, _arg(k_new, torch.bfloat16, shape, device, "k_new"),
+                                _arg(v_new, torch.bfloat16, shape, device, "v_new"), n, _stream(stream)),
+           "wm_kvq_append")
+
+
+def kvq_read(cache: KVQCache, n: int, k_out=None, v_out=None, stream=None):
+    """The values of the last n positions as bf16: (k, v), each [B, n, Hkv, D]."""
+    device = _kvq_device(cache)
+    shape = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = _new_on(stream, shape, torch.bfloat16, device)
+    if v_out is None:
+        v_out = _new_on(stream, shape, torch.bfloat16, device)
+    _check(load().wm_kvq_read(cache._ref, n, _arg(k_out, torch.bfloat16, shape, device, "k_out"),
+                              _arg(v_out, torch.bfloat16, shape, device, "v_out"), _stream(stream)), "wm_kvq_read")
+    return k_out, v_out
+
+
+def kvq_workspace_size(batch: int, n_kv_heads: int, n_q_heads: int, n_q: int, head_dim: int) -> int:
+    n = load().wm_kvq_workspace_size(batch, n_kv_heads, n_q_heads, n_q, head_dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise WmError(WM_ERR_INVALID_ARG, "wm_kvq_workspace_size")
+    return int(n)
+
+
+def kvq_workspace(cache: KVQCache, n_q_heads: int, n_q: int) -> torch.Tensor:
+    """A workspace for verify_attn_kvq on this cache; calls that can overlap on the GPU need one each."""
+    need = kvq_workspace_size(cache.batch, cache.n_kv_heads, n_q_heads, n_q, cache.head_dim)
+    return torch.empty(need, dtype=torch.uint8, device=cache.data.device)
+
+
+def verify_attn_kvq(cache: KVQCache, q: torch.Tensor, scale: float, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [B, T, Hq, D] over a 4-bit cache (T = 1: single-token
+    decode); returns (out bf16, lse fp32)."""
+    device = _kvq_device(cache)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, T, Hq, D], got {tuple(q.shape)}")
+    T, Hq = q.shape[1], q.shape[2]
+    shape = (cache.batch, T, Hq, cache.head_dim)
+    qp = _arg(q, torch.bfloat16, shape, device, "q")
+    if out is None:
+        out = _new_on(stream, shape, torch.bfloat16, device)
+    if lse is None:
+        lse = _new_on(stream, shape[:3], torch.float32, device)
+    if workspace is None:
+        need = kvq_workspace_size(cache.batch, cache.n_kv_heads, Hq, T, cache.head_dim)
+        workspace = _new_on(stream, (-(-need // 4),), torch.float32, device)
+    elif workspace.get_device() != device:
+        raise ValueError(f"workspace must be on the current device (cuda:{device}), is on {workspace.device}")
+    _check(load().wm_verify_attn_kvq(cache._ref, qp, T, Hq, float(scale),
+                                     _arg(out, torch.bfloat16, shape, device, "out"),
+                                     _arg(lse, torch.float32, shape[:3], device, "lse"), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(stream)),
+           "wm_verify_attn_kvq")
+    return out, lse
+
+
+def spec_accept(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, draft_tokens: torch.Tensor,
+                u_accept: torch.Tensor, u_sample: torch.Tensor, n_draft: torch.Tensor | None = None,
+                seq_lens: torch.Tensor | None = None, tokens=None, n_accepted=None, new_len=None, stream=None):
+    """Verify drafted tokens [B, k] int32 against the target's probabilities
+    [B, k + 1, V] fp32 from given uniforms (u_accept [B, k], u_sample [B]);
+    draft_probs [B, k, V] or None for drafts without probabilities.  Returns
+    (tokens [B, k + 1] int32, n_accepted [B] int32, new_len [B] int64); new_len --
+    what ring_rollback takes -- is None without ``seq_lens`` [B] int64, the cache
+    lengths with the k + 1 verified positions.  See wm_spec_accept in include/wm_api.h."""
+    device = torch.cuda.current_device()
+    if target_probs.dim() != 3 or draft_tokens.dim() != 2:
+        raise ValueError("target_probs must be [B, k + 1, V] and draft_tokens [B, k]")
+    B, k = draft_tokens.shape
+    V = target_probs.shape[2]
+    f32, i32, i64 = torch.float32, torch.int32, torch.int64
+    pp = _arg(target_probs, f32, (B, k + 1, V), device, "target_probs")
+    qp = _arg(draft_probs, f32, (B, k, V), device, "draft_probs") if draft_probs is not None else None
+    xp = _arg(draft_tokens, i32, (B, k), device, "draft_tokens")
+    np_ = _arg(n_draft, i32, (B,), device, "n_draft") if n_draft is not None else None
+    sp = _arg(seq_lens, i64, (B,), device, "seq_lens") if seq_lens is not None else None
+    if new_len is not None and seq_lens is None:
+        raise ValueError("new_len needs seq_lens")
+    if tokens is None:
+        tokens = _new_int(stream, (B, k + 1), i32, device)
+    if n_accepted is None:
+        n_accepted = _new_int(stream, (B,), i32, device)
+    if new_len is None and seq_lens is not None:
+        new_len = _new_int(stream, (B,), i64, device)
+    _check(load().wm_spec_accept(pp, qp, xp, np_, _arg(u_accept, f32, (B, k), device, "u_accept"),
+                                 _arg(u_sample, f32, (B,), device, "u_sample"), sp, B, k, V,
+                                 _arg(tokens, i32, (B, k + 1), device, "tokens"),
+                                 _arg(n_accepted, i32, (B,), device, "n_accepted"),
+                                 _arg(new_len, i64, (B,), device, "new_len") if new_len is not None else None,
+                                 _stream(stream)), "wm_spec_accept")
+    return tokens, n_accepted, new_len
 
 
 def set_draft_math(math: int) -> None:
