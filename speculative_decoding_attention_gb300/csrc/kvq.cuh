@@ -186,7 +186,10 @@ struct KvqWalk {
     }
 };
 
-cudaError_t launch_kvq_attn(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
+// The attention grid per head_dim (attn_kvq_d<D>.cu), and the merge of its parts.
+cudaError_t launch_kvq_attn_d64(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
+cudaError_t launch_kvq_attn_d128(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
+cudaError_t launch_kvq_attn_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_merge(const KvqAttnParams &p, cudaStream_t stream);
 
 cudaError_t launch_kvq_append(const KvqView &c, const void *k_new, const void *v_new, int n_new, int32_t *err,

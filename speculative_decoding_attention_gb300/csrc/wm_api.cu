@@ -883,7 +883,9 @@ wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32
     p.wait_limit = t_wait_limit;
     p.stall_tile = t_stall_tile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_kvq_attn(p, n_cta, st);
+    const cudaError_t e = kv->head_dim == 64    ? launch_kvq_attn_d64(p, n_cta, st)
+                          : kv->head_dim == 128 ? launch_kvq_attn_d128(p, n_cta, st)
+                                                : launch_kvq_attn_d256(p, n_cta, st);
     if (e != cudaSuccess) return WM_ERR_CUDA;
     return launch_status(launch_kvq_merge(p, st));
 }
