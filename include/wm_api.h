@@ -446,10 +446,10 @@ wm_status wm_kvq_read(const wm_kvq *kv, int32_t n, void *k_out, void *v_out, voi
  *   workspace  wm_kvq_workspace_size(...) bytes, 256-byte aligned; no initial
  *              contents.  Calls that can overlap on the GPU need one each.
  * The work is split on the device from the actual lengths: one CTA per SM takes
- * an equal run of the batch's 128-position tiles.  Two launches.  Results do
+ * an equal run of the batch's 256-position tiles.  Two launches.  Results do
  * not depend on what else runs: repeated calls are bit-identical.
  * At most 64 rows (n_q * n_q_heads / n_kv_heads) per KV head and 2^30 tiles
- * (batch * n_kv_heads * ceil(capacity / 128)); WM_ERR_UNSUPPORTED beyond.
+ * (batch * n_kv_heads * ceil(capacity / 256)); WM_ERR_UNSUPPORTED beyond.
  */
 wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32_t n_q_heads, float scale, void *out,
                              float *lse, void *workspace, size_t workspace_bytes, void *stream);

@@ -84,7 +84,7 @@ struct KvqAttnParams {
     int32_t stall_tile;  // tests of the timeout path only, else -1
 };
 
-constexpr int kKvqTile = 128;  // positions per attention tile: two records
+constexpr int kKvqTile = 256;  // positions per attention tile: two sub-tiles of two records
 
 __device__ __forceinline__ int kvq_tiles(const KvqView &c, int b) {
     return (int)((kvq_len(c, b) + kKvqTile - 1) / kKvqTile);
