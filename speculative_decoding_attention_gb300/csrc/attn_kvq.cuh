@@ -18,13 +18,14 @@
 //   t_jr = S_jr a_j + zq_r b_j + ls_j,  a = s_K 2^24 f,  b = z_K f,  f = scale log2(e)
 //   zq_r = sum_d q_rd,  ls_j = log2(s_V).
 // V's scale is folded into the weight: P'_jr = 2^(t_jr - m_r) = s_Vj p_jr, so that
-//   o_r = [ 2^24 sum_j P'_jr c_j  +  sum_j P'_jr (z_V / s_V)_j ] / sum_j P'_jr (1 / s_V)_j
+//   o_r = [ 2^24 sum_j P'_jr (c_j - 8) + sum_j P'_jr (z_V / s_V + 8)_j ] / sum_j P'_jr (1 / s_V)_j
 // with the running maximum m taken over t: the largest P' is near the top of fp16's
-// range whatever the scales are.  P' goes to the tensor cores as two fp16 parts,
-// hi = fp16(P') and lo = fp16(P' - hi), accumulated into the same O: its rounding is
-// 2^-22 of it.  (One part would be off by 2^-11, and as s c and z are large beside
-// their sum that shows in the output wherever they cancel.)  A row of constant values
-// has s_V = 0 and codes 0; a stand-in scale |z| / 256 carries its zero.
+// range whatever the scales are.  P' is rounded to fp16 for the first sum only (at
+// most 2^-11 of it; the others are fp32 sums of P' as it is).  That error is weighted
+// by s_V (c - 8), about the value itself: with c in its place it would be weighted by the
+// value's distance from the zero, which shows wherever values cancel.  The - 8 is
+// a product with a constant operand, free on the tensor cores.  A row of constant
+// values has s_V = 0 and codes 0; a stand-in scale |z| / 256 carries its zero.
 //
 // Each CTA takes one run of the batch's tiles (kvq_schedule), cut into parts at
 // (sequence, KV head) borders; every role counts tiles across parts, so no
@@ -59,23 +60,36 @@ struct KvqCfg {
     static constexpr int STAGE = 2 * REC;               // a sub-tile of 128 keys
     static constexpr int NC = D == 256 ? 2 : 1;         // 128-channel chunks
     static constexpr int KU = D == 64 ? 2 : 4;          // 16-byte units per key and chunk
-    static constexpr int ND = NR <= 32 ? 8 : 4;         // converting warps
-    static constexpr int HR = NR <= 48 ? 8 : 16;        // rows per softmax warp
+    // Rows per softmax warp and converting warps.  More warps hide more latency, fewer leave
+    // more registers to each and repeat less per-key work; measured in us, chosen form first:
+    // up to 16 rows at head_dim 128 (ragged batch of 2.4 GB) 16 warps 463, 12 531, 8 549; 32
+    // rows at head_dim 256 (1M positions) 4 warps 140, 8 158; at 128 (128K) 4 warps 37.2, 8
+    // 38.4, and 16 rows per softmax warp instead of 8 42; 48 rows (2 x 1M) 16 rows per
+    // softmax warp and 4 converting 662, 8 and 4 996, 16 and 8 963.
+    static constexpr int HR = NR <= 32 ? 8 : 16;
+    static constexpr int ND = NR == 16 ? (D == 128 ? 16 : 8) : 4;
+    static constexpr int KG = ND == 16 ? 2 : 1, VG = KG;  // warp groups for K and V
+    // Two groups take turns, each with slots of its own (a wait on a slot's barrier has to
+    // follow every use of it).
+    static_assert(KG == 1 || NC == 1, "a group owns its slots");
+    static_assert(HR == 8 || HR == 16, "rows per softmax warp");
     static constexpr int NSW = 4 * (NR / HR);           // softmax warps
     static constexpr int W_D = 3, W_S = 3 + ND;         // first converting and first softmax warp
     static constexpr int THREADS = 32 * (W_S + NSW);
-    // tensor memory: two K and two V code slots of 64 columns, S twice, O
-    static constexpr int S_COL = 256, O_COL = 256 + 2 * NR;
-    static_assert(O_COL + NC * NR <= 512, "tensor memory");
+    // tensor memory: K and V code slots of 64 columns, the constant -8 (8 columns), S of two sub-tiles, O
+    static constexpr int SLOTS = (512 - 8 - 2 * NR - NC * NR) / 64;
+    static constexpr int KS = 2, VS = SLOTS >= 6 ? 4 : SLOTS >= 4 ? 2 : 1;
+    static constexpr int V_COL = 64 * KS, S_COL = 64 * (KS + VS), O_COL = S_COL + 2 * NR, E_COL = O_COL + NC * NR;
+    static_assert(VS >= 1 && E_COL + 8 <= 512, "tensor memory");
     // shared memory
     static constexpr int PT_ROW = NR <= 16 ? 32 : NR <= 32 ? 64 : 128;
     static constexpr uint32_t PT_SWIZZLE = NR <= 16 ? tc::SWIZZLE_32B : NR <= 32 ? tc::SWIZZLE_64B : tc::SWIZZLE_128B;
     static constexpr int PT_ATOM = 8 * PT_ROW, PT_BYTES = 128 * PT_ROW;  // one part of one sub-tile
-    static constexpr int PB_BYTES = 4 * PT_BYTES;       // one P' buffer: two sub-tiles, hi and lo
+    static constexpr int PB_BYTES = 2 * PT_BYTES;       // one P' buffer: two sub-tiles
     static constexpr int Q_REGION = NR * 128;           // 64 channels of every row
     static constexpr int Q_OFF = 0;
     static constexpr int PT_OFF = Q_OFF + (D / 64) * Q_REGION;
-    // behind the stages: constants of four sub-tiles, per-row scratch, barriers
+    // behind the stages: per-key constants, per-row scratch, barriers
     static constexpr int CONST_BYTES = 4 * 128 * 20;
     static constexpr int RED_BYTES = 8 * NR * 4, ROW_BYTES = 2 * NR * 4;
     static constexpr int TAIL = CONST_BYTES + RED_BYTES + 2 * ROW_BYTES + 256 + 512 + 32 * 8 + 64;
@@ -93,7 +107,7 @@ struct KvqCfg {
     static constexpr int NM_OFF = ZQ_OFF + ROW_BYTES;             // float [2][NR]: minus (running maximum - kKvqOff)
     static constexpr int FLAG_OFF = NM_OFF + ROW_BYTES;           // int [64]: [0] abort, [8 + w] scratch
     static constexpr int BAR_OFF = FLAG_OFF + 256;
-    static constexpr int NBAR = 2 * NST + 4 + 4 + 1 + 1 + 2 + 2 + 1 + 2;
+    static constexpr int NBAR = 2 * NST + 8 + 8 + 1 + 1 + 2 + 2 + 1 + 2;
     static_assert(NBAR * 8 <= 512, "barriers");
     static constexpr int WARP_OFF = BAR_OFF + 512;                // int64 [32] + int4 of the schedule
     static constexpr int TPTR_OFF = WARP_OFF + 32 * 8 + 16;
@@ -166,6 +180,15 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+// Two pairs of fp32.
+__device__ __forceinline__ ulonglong2 ld_shared_pairs(uint32_t addr) {
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) { st_shared_u32(addr, __float_as_uint(v)); }
+
 // D[tmem] (+)= A[tmem] * B[smem desc], fp16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -203,7 +226,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // Rest of a wait whose first poll failed.  Gives up after `limit` polls, or once another
 // role has given up: records the timeout, raises the abort flag and returns false.
-static __device__ __noinline__ bool kvq_wait_slow(uint32_t bar, uint32_t parity, uint32_t limit, volatile int *flags,
+__device__ __forceinline__ bool kvq_wait_slow(uint32_t bar, uint32_t parity, uint32_t limit, volatile int *flags,
                                            int32_t *err) {
     for (uint32_t i = 0; i < limit; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -225,18 +248,18 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     uint8_t *gb = smem_raw + (sbase - raw);
     const uint32_t sQ = sbase + C::Q_OFF, sPT = sbase + C::PT_OFF, sST = sbase + C::ST_OFF;
-    float *red = reinterpret_cast<float *>(gb + C::RED_OFF);  // [2][4][NR]
-    float *s_zq = reinterpret_cast<float *>(gb + C::ZQ_OFF);  // [2][NR]
-    float *s_nm = reinterpret_cast<float *>(gb + C::NM_OFF);  // [2][NR]
-    float4 *s_const = reinterpret_cast<float4 *>(gb + C::CONST_OFF);                     // [4][128]
-    float *s_zr = reinterpret_cast<float *>(gb + C::CONST_OFF + 4 * 128 * 16);           // [4][128]
+    const uint32_t s_red = sbase + C::RED_OFF;              // float [2][4][NR]
+    const uint32_t s_zq = sbase + C::ZQ_OFF;                // float [2][NR]
+    const uint32_t s_nm = sbase + C::NM_OFF;                // float [2][NR]
+    const uint32_t s_const = sbase + C::CONST_OFF;          // float4 [4][128]
+    const uint32_t s_zr = s_const + 4 * 128 * 16;           // float [4][128]
     volatile int *flags = reinterpret_cast<volatile int *>(gb + C::FLAG_OFF);
     const uint32_t bars = sbase + C::BAR_OFF;
     const uint32_t bar_full = bars;                      // [NST] stage landed
     const uint32_t bar_empty = bar_full + 8 * NST;       // [NST] stage read by everyone
-    const uint32_t bar_aready = bar_empty + 8 * NST;     // [4] code slot written (K, K, V, V)
-    const uint32_t bar_afree = bar_aready + 32;          // [4] code slot consumed
-    const uint32_t bar_sfull = bar_afree + 32;           // S of tile t
+    const uint32_t bar_aready = bar_empty + 8 * NST;     // [KS + VS] code slot written
+    const uint32_t bar_afree = bar_aready + 64;          // [KS + VS] code slot consumed
+    const uint32_t bar_sfull = bar_afree + 64;           // S of tile t
     const uint32_t bar_sfree = bar_sfull + 8;
     const uint32_t bar_pfull = bar_sfree + 8;            // [2] P' of tile t, buffer t % NPB
     const uint32_t bar_odone = bar_pfull + 16;           // [2] its P.V
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 8);  // K and V conversion, four warps each
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < C::KS + C::VS; ++i) {
             mbar_init(bar_aready + 8 * i, 4);
             mbar_init(bar_afree + 8 * i, 1);
         }
@@ -269,6 +292,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
         for (int i = 0; i < 64; ++i) flags[i] = 0;
         fence_mbar_init();
     }
+    static_assert(C::KS + C::VS <= 8, "slot barriers");
     if (warp == 1) {
         tc::tmem_alloc(smem_u32(tptr), 512);
         tc::tmem_relinquish();
@@ -277,6 +301,17 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tptr;
+
+    // The constant operand -8: for the 16 keys of one MMA, pairs of -8 2^-24 and -8 2^-20.
+    if (warp >= C::W_D && warp < C::W_D + 4) {
+        const uint32_t v0 = 0x80088008u, v1 = 0x80808080u;
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %1, %2, %1, %2, %1, %2};" ::"r"(
+                         tmem + ((uint32_t)(32 * (warp & 3)) << 16) + C::E_COL),
+                     "r"(v0), "r"(v1)
+                     : "memory");
+        tc::wait_st();
+        tc::fence_before_sync();  // seen by the issuer through the first code slot's barrier
+    }
 
     pdl_wait();
     pdl_launch_dependents();
@@ -367,8 +402,8 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
-                            const int u = (2 * gt + j) * NC + c, slot = u & 1;
-                            ok = ok && wait(bar_aready + 8 * slot, u >> 1);
+                            const int u = (2 * gt + j) * NC + c, slot = u % C::KS;
+                            ok = ok && wait(bar_aready + 8 * slot, u / C::KS);
                             if (!ok) break;
                             tc::fence_after_sync();
                             const uint32_t a = tmem + 64 * slot, d = tmem + C::S_COL + j * NR;
@@ -403,22 +438,21 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     ok = wait(bar_pfull + 8 * buf, gt / NPB);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const uint64_t hi = p_desc + ((buf * C::PB_BYTES + 2 * j * C::PT_BYTES) >> 4);
-                        const uint64_t lo = hi + (C::PT_BYTES >> 4);
+                        const uint64_t pb = p_desc + ((buf * C::PB_BYTES + j * C::PT_BYTES) >> 4);
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
-                            const int u = (2 * gt + j) * NC + c, slot = u & 1;
-                            ok = ok && wait(bar_aready + 16 + 8 * slot, u >> 1);
+                            const int u = (2 * gt + j) * NC + c, slot = u % C::VS;
+                            ok = ok && wait(bar_aready + 8 * (C::KS + slot), u / C::VS);
                             if (!ok) break;
                             tc::fence_after_sync();
-                            const uint32_t a = tmem + 128 + 64 * slot, d = tmem + C::O_COL + c * NR;
+                            const uint32_t a = tmem + C::V_COL + 64 * slot, d = tmem + C::O_COL + c * NR;
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {  // 16 keys each
-                                mma_f16_ts(d, a + 8 * kk, hi + ((kk * 2 * C::PT_ATOM) >> 4), id_pv,
-                                           t > 0 || j > 0 || kk > 0);
-                                mma_f16_ts(d, a + 8 * kk, lo + ((kk * 2 * C::PT_ATOM) >> 4), id_pv, 1u);
+                                const uint64_t bp = pb + ((kk * 2 * C::PT_ATOM) >> 4);
+                                mma_f16_ts(d, a + 8 * kk, bp, id_pv, t > 0 || j > 0 || kk > 0);
+                                mma_f16_ts(d, tmem + C::E_COL, bp, id_pv, 1u);
                             }
-                            tc::commit(bar_afree + 16 + 8 * slot);
+                            tc::commit(bar_afree + 8 * (C::KS + slot));
                         }
                     }
                     if (ok) tc::commit(bar_odone + 8 * buf);
@@ -434,21 +468,21 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
         const int L = 32 * q4 + lane;  // tensor-memory lane: key (K), channel of a chunk (V)
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
 
-        // One slot of 64 columns from a sub-tile's stage.
-        const auto fill = [&](int u, int slot, auto &&unit_addr, int units, bool live) {
-            if (u >= 2) wait(bar_afree + 8 * slot, (u >> 1) - 1);
+        // A chunk's units of this lane are all loaded before the first is converted, so
+        // that one latency of shared memory is paid.
+        const auto convert = [&](const uint4 (&x)[4], int units, int slot, int use, bool live) {
+            if (use > 0) wait(bar_afree + 8 * slot, use - 1);
             __syncwarp();
             tc::fence_after_sync();
             if (live) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (j < units)
-                        kvq_unit_to_tmem(tmem + lane_off + 64 * slot + 16 * j, ld_shared_v4(unit_addr(j)));
-                tc::wait_st();
+                    if (j < units) kvq_unit_to_tmem(tmem + lane_off + 64 * slot + 16 * j, x[j]);
             }
-            tc::fence_before_sync();
         };
         const auto ready = [&](int slot) {
+            tc::wait_st();
+            tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_aready + 8 * slot);
         };
@@ -458,65 +492,75 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             const uint32_t unit = rec + (L & 63) * 16;
             const uint32_t ksz = ld_shared_u32(rec + rec_ks_off(D) + (L & 63) * 4);
             const uint32_t vsz = ld_shared_u32(rec + rec_vs_off(D) + (L & 63) * 4);
-            // Constants of this key.  Slot st % 4 is free once its code slot is: sub-tile
-            // st - 4's were read before S of the tile after it was issued, and the code
-            // slot waits for that S or a later one.
-            const float ks = __uint_as_float(ksz << 16), kz = __uint_as_float(ksz & 0xffff0000u);
-            const float vs = __uint_as_float(vsz << 16), vz = __uint_as_float(vsz & 0xffff0000u);
-            // Scale 0 (constant values, codes 0): a stand-in that keeps z / s in
-            // range.  At least 2^-90, which keeps the sums of P' / s below fp32's
-            // largest: values are off by 15 x 2^-90 where a scale is smaller.
-            const float se = fmaxf(vs > 0.f ? vs : fabsf(vz) * 0.00390625f, 8.0779357e-28f);
-            const bool by16 = L & 2;  // this key's V codes are 16 times too large: P' is divided by 16
-            float inv = rcp(se) * (by16 ? 16.f : 1.f), zr = vz * inv;
-            const bool bad = !(fabsf(ks) < CUDART_INF_F && fabsf(kz) < CUDART_INF_F && vs >= 0.f &&
-                               vs < CUDART_INF_F && fabsf(zr) < CUDART_INF_F);
-            // not finite: NaN in the logit reaches every row that sees this key, and only
-            // those (a weight of 0 times these is 0)
-            if (bad) inv = zr = 0.f;
-            const float4 kc = make_float4(ks * 16777216.f, kz, bad ? CUDART_NAN_F : lg2(se) - (by16 ? 4.f : 0.f), inv);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int u = st * NC + c;
-                fill(u, u & 1, [&](int j) { return unit + (c * 4 + j) * 1024; }, C::KU, true);
+                uint4 x[4];
+#pragma unroll
+                for (int j = 0; j < C::KU; ++j) x[j] = ld_shared_v4(unit + (c * 4 + j) * 1024);
+                convert(x, C::KU, u % C::KS, u / C::KS, true);
                 if (c == 0) {
-                    s_const[(st & 3) * 128 + L] = kc;
-                    s_zr[(st & 3) * 128 + L] = zr;
+                    // Constants of this key.  Slot st % 4 is free once the code slot is: sub-tile
+                    // st - 4's were read before S of the tile after it was issued, and the code
+                    // slot waits for that S or a later one.
+                    const float ks = __uint_as_float(ksz << 16), kz = __uint_as_float(ksz & 0xffff0000u);
+                    const float vs = __uint_as_float(vsz << 16), vz = __uint_as_float(vsz & 0xffff0000u);
+                    // Scale 0 (constant values, codes 0): a stand-in that keeps z / s in
+                    // range.  At least 2^-90, which keeps the sums of P' / s below fp32's
+                    // largest: values are off by 15 x 2^-90 where a scale is smaller.
+                    const float se = fmaxf(vs > 0.f ? vs : fabsf(vz) * 0.00390625f, 8.0779357e-28f);
+                    const bool by16 = L & 2;  // this key's V codes are 16 times too large: P' is divided by 16
+                    const float up = by16 ? 16.f : 1.f;
+                    float inv = rcp(se) * up, zr = fmaf(vz, inv, 8.f * up);
+                    const bool bad = !(fabsf(ks) < CUDART_INF_F && fabsf(kz) < CUDART_INF_F && vs >= 0.f &&
+                                       vs < CUDART_INF_F && fabsf(zr) < CUDART_INF_F);
+                    // not finite: NaN in the logit reaches every row that sees this key, and only
+                    // those (a weight of 0 times these is 0)
+                    if (bad) inv = zr = 0.f;
+                    const float ls = bad ? CUDART_NAN_F : lg2(se) - (by16 ? 4.f : 0.f);
+                    st_shared_v4(s_const + ((st & 3) * 128 + L) * 16,
+                                 make_uint4(__float_as_uint(ks * 16777216.f), __float_as_uint(kz), __float_as_uint(ls),
+                                            __float_as_uint(inv)));
+                    st_shared_f32(s_zr + ((st & 3) * 128 + L) * 4, zr);
                 }
-                ready(u & 1);
+                ready(u % C::KS);
             }
             if (lane == 0) mbar_arrive(bar_empty + 8 * (st % NST));
         };
         const auto do_v = [&](int st) {
+            // head_dim 64: lanes 64..127 have no channel; their rows of O are never read
+            const bool live = D > 64 || q4 < 2;
             wait(bar_full + 8 * (st % NST), st / NST);
             const uint32_t unit = sST + (st % NST) * C::STAGE + rec_v_off(D) + L * 16;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int u = st * NC + c;
-                // head_dim 64: lanes 64..127 have no channel; their rows of O are never read
-                fill(u, 2 + (u & 1),
-                     [&](int j) { return unit + c * 2048 + (j >> 1) * C::REC + (j & 1) * 16 * D; }, 4, D > 64 || q4 < 2);
-                ready(2 + (u & 1));
+                uint4 x[4];
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = ld_shared_v4(unit + c * 2048 + (j >> 1) * C::REC + (j & 1) * 16 * D);
+                }
+                convert(x, 4, C::KS + u % C::VS, u / C::VS, live);
+                ready(C::KS + u % C::VS);
             }
             if (lane == 0) mbar_arrive(bar_empty + 8 * (st % NST));
         };
+        // (Once the pipeline is given up every wait returns at once, and the loops run out.)
         const int n_sub = 2 * n_all;
-        if constexpr (ND == 8) {
-            for (int st = 0; st < n_sub && !__any_sync(0xffffffffu, flags[0]); ++st) {
-                if (dw < 4)
-                    do_k(st);
-                else
-                    do_v(st);
-                __syncwarp();
-            }
+        if constexpr (ND > 4) {
+            const int grp = dw >> 2;
+            if (grp < C::KG)
+                for (int st = grp; st < n_sub; st += C::KG) do_k(st);
+            else
+                for (int st = grp - C::KG; st < n_sub; st += C::VG) do_v(st);
         } else {
             // one group: the next tile's K before this tile's V, so that S runs ahead
             do_k(0);
             do_k(1);
-            for (int st = 0; st < n_sub && !__any_sync(0xffffffffu, flags[0]); ++st) {
+            for (int st = 0; st < n_sub; ++st) {
                 if (st + 2 < n_sub) do_k(st + 2);
                 do_v(st);
-                __syncwarp();
             }
         }
     } else {
@@ -567,7 +611,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             for (int w = 0; w < NSW; ++w) top = max(top, (uint32_t)flags[8 + w]);
             const int ex = top == 0 ? 0 : min(100, max(-100, (int)(top >> 7) - 127 - 14));
             const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-            if (ct < NR) s_nm[(part & 1) * NR + ct] = 0.f;
+            if (ct < NR) st_shared_f32(s_nm + ((part & 1) * NR + ct) * 4, 0.f);
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 const int idx = ct + 32 * NSW * k, r = idx / VPR, v = idx % VPR;
@@ -587,7 +631,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 st_shared_v4(sQ + (v >> 3) * C::Q_REGION + swz128(r, v & 7), make_uint4(o[0], o[1], o[2], o[3]));
 #pragma unroll
                 for (int o2 = VPR / 2; o2; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-                if (v == 0) s_zq[(part & 1) * NR + r] = sum;
+                if (v == 0) st_shared_f32(s_zq + ((part & 1) * NR + r) * 4, sum);
             }
             fence_proxy_async_smem();
             named_bar_sync(1, 32 * NSW);  // sums and maxima visible
@@ -597,23 +641,20 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 
         int b = 0, h = 0, t0 = 0, n = 0, g = 0, part = 0;
         bool have = walk.next(p.c, b, h, t0, n);
-        float f = have ? stage_q(b, h, 0) * p.scale_log2 : 0.f, f_next = 0.f;
+        float f = have ? stage_q(b, h, 0) * p.scale_log2 : 0.f;
         while (have) {
-            const int64_t len = kvq_len(p.c, b);
-            const int64_t k_begin = (int64_t)t0 * TK;
-            const int64_t k_end = min(k_begin + (int64_t)n * TK, len);
-            const int64_t qpos0 = len - p.n_q;
-            int nb = 0, nh = 0, nt0 = 0, nn = 0;
-            const bool have_next = walk.next(p.c, nb, nh, nt0, nn);
-            const float *zq = s_zq + (part & 1) * NR + r0;
-            float *nm = s_nm + (part & 1) * NR + r0;
+            // positions fit 32 bits (the capacity does)
+            const int len = (int)kvq_len(p.c, b);
+            const int key_first = t0 * TK, key_end = (int)min((int64_t)(t0 + n) * TK, (int64_t)len);
+            const int qpos0 = len - p.n_q;
+            const uint32_t zq = s_zq + ((part & 1) * NR + r0) * 4, nm = s_nm + ((part & 1) * NR + r0) * 4;
 
             uint64_t l2[HR / 2], z2[HR / 2];  // sums of P' / s_V and P' z_V / s_V, two rows each
 #pragma unroll
             for (int i = 0; i < HR / 2; ++i) l2[i] = z2[i] = 0;
             for (int t = 0; t < n; ++t) {
                 const int gt = g + t;
-                const int64_t key0 = k_begin + (int64_t)t * TK;
+                const int key0 = key_first + t * TK;
 
                 wait(bar_sfull, gt);
                 __syncwarp();
@@ -627,86 +668,80 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     else
                         tc::ld_32x32b_x8(at, s[j]);
                 }
-                float4 kc[2];
-                float zr[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    kc[j] = s_const[((2 * gt + j) & 3) * 128 + kt];
-                    zr[j] = s_zr[((2 * gt + j) & 3) * 128 + kt];
-                }
                 tc::wait_ld();
                 tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_sfree);
 
                 // t - m of every row
-                uint64_t a2[2], b2[2], ls2[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    a2[j] = pack2(kc[j].x * f, kc[j].x * f);
-                    b2[j] = pack2(kc[j].y * f, kc[j].y * f);
-                    ls2[j] = pack2(kc[j].z, kc[j].z);
-                }
-                float top = -CUDART_INF_F;
+                    const uint4 kc = ld_shared_v4(s_const + (((2 * gt + j) & 3) * 128 + kt) * 16);
+                    const float a = __uint_as_float(kc.x) * f, bz = __uint_as_float(kc.y) * f;
+                    const uint64_t a2 = pack2(a, a), b2 = pack2(bz, bz);
+                    const uint64_t ls2 = pack2(__uint_as_float(kc.z), __uint_as_float(kc.z));
 #pragma unroll
-                for (int i = 0; i < HR; i += 4) {
-                    const ulonglong2 z4 = *reinterpret_cast<const ulonglong2 *>(zq + i);
-                    const ulonglong2 m4 = *reinterpret_cast<const ulonglong2 *>(nm + i);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
+                    for (int i = 0; i < HR; i += 4) {
+                        const ulonglong2 z4 = ld_shared_pairs(zq + 4 * i), m4 = ld_shared_pairs(nm + 4 * i);
                         float *x = s[j] + i;
-                        unpack2(fma2(pack2(x[0], x[1]), a2[j], fma2(z4.x, b2[j], add2(ls2[j], m4.x))), x[0], x[1]);
-                        unpack2(fma2(pack2(x[2], x[3]), a2[j], fma2(z4.y, b2[j], add2(ls2[j], m4.y))), x[2], x[3]);
+                        unpack2(fma2(pack2(x[0], x[1]), a2, fma2(z4.x, b2, add2(ls2, m4.x))), x[0], x[1]);
+                        unpack2(fma2(pack2(x[2], x[3]), a2, fma2(z4.y, b2, add2(ls2, m4.y))), x[2], x[3]);
                     }
                 }
-                if (key0 + TK > k_end || key0 + TK - 1 > qpos0) {
-                    // row r sees key kabs iff kabs < k_end and kabs <= qpos0 + r / group
+                float inv[2], zr[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    inv[j] = ld_shared_f32(s_const + (((2 * gt + j) & 3) * 128 + kt) * 16 + 12);
+                    zr[j] = ld_shared_f32(s_zr + (((2 * gt + j) & 3) * 128 + kt) * 4);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_sfree);  // S and the constants are read
+                if (key0 + TK > key_end || key0 + TK - 1 > qpos0) {
+                    // row r sees a key iff it is below key_end and at most qpos0 + r / group
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int64_t kabs = key0 + 128 * j + kt;
-                        const int64_t first = kabs - qpos0;  // first query position that sees the key
+                        const int key = key0 + 128 * j + kt;
+                        // first row that sees it: query position key - qpos0, if that is not before the first
+                        const int row = key >= key_end ? NR : min(max(key - qpos0, 0), NR) * p.group;
 #pragma unroll
                         for (int i = 0; i < HR; ++i)
-                            if (kabs >= k_end || first > (r0 + i) / p.group) s[j][i] = -CUDART_INF_F;
+                            if (r0 + i < row) s[j][i] = -CUDART_INF_F;
                     }
                 }
+                float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
-                for (int i = 0; i < HR; ++i) top = fmaxf(top, fmaxf(s[0][i], s[1][i]));
+                for (int i = 1; i < HR; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
                 const bool raise = named_bar_sync_or(2 + grp, 128, top > kKvqOff + kKvqRaise);
                 if (raise || t == 0) {
                     // Raise the maxima of this group's rows (at the part's first tile: set them).
 #pragma unroll
                     for (int i = 0; i < HR; ++i) {
                         const float mx = warp_max_f(fmaxf(s[0][i], s[1][i]));
-                        if (lane == 0) red[NR * q4 + r0 + i] = mx;
+                        if (lane == 0) st_shared_f32(s_red + (NR * q4 + r0 + i) * 4, mx);
                     }
                     named_bar_sync(2 + grp, 128);
-                    float up[HR];
+                    // by how much row i's maximum goes up
+                    const auto up = [&](int i) -> float {
+                        const uint32_t x = s_red + (r0 + i) * 4;
+                        const float mx = fmaxf(fmaxf(ld_shared_f32(x), ld_shared_f32(x + 4 * NR)),
+                                               fmaxf(ld_shared_f32(x + 8 * NR), ld_shared_f32(x + 12 * NR))) - kKvqOff;
+                        return t > 0 ? fmaxf(mx, 0.f) : mx == -CUDART_INF_F ? 0.f : mx;
+                    };
 #pragma unroll
                     for (int i = 0; i < HR; ++i) {
-                        const float *x = red + r0 + i;
-                        const float mx = fmaxf(fmaxf(x[0], x[NR]), fmaxf(x[2 * NR], x[3 * NR])) - kKvqOff;
-                        up[i] = t == 0 ? (mx == -CUDART_INF_F ? 0.f : mx) : fmaxf(mx, 0.f);
-                        s[0][i] -= up[i];
-                        s[1][i] -= up[i];
+                        const float d = up(i);
+                        s[0][i] -= d;
+                        s[1][i] -= d;
                     }
-                    if (q4 == 0) {
-#pragma unroll
-                        for (int i = 0; i < HR; ++i)
-                            if (lane == i) nm[i] -= up[i];
-                    }
-                    named_bar_sync(2 + grp, 128);
+                    if (q4 == 0 && lane < HR) st_shared_f32(nm + 4 * lane, ld_shared_f32(nm + 4 * lane) - up(lane));
                     if (t > 0) {
                         // O holds this part's tiles so far at the old maxima
                         wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
                         __syncwarp();
                         tc::fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < HR; ++i) up[i] = ex2(-up[i]);
-#pragma unroll
                         for (int i = 0; i < HR / 2; ++i) {
-                            l2[i] = mul2(l2[i], pack2(up[2 * i], up[2 * i + 1]));
-                            z2[i] = mul2(z2[i], pack2(up[2 * i], up[2 * i + 1]));
+                            const uint64_t al = pack2(ex2(-up(2 * i)), ex2(-up(2 * i + 1)));
+                            l2[i] = mul2(l2[i], al);
+                            z2[i] = mul2(z2[i], al);
                         }
 #pragma unroll
                         for (int c = 0; c < NC; ++c)
@@ -717,22 +752,23 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                                 tc::ld_32x32b_x8(at, v8);
                                 tc::wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v8[i] *= up[8 * j + i];
+                                for (int i = 0; i < 8; ++i) v8[i] *= ex2(-up(8 * j + i));
                                 tc::st_32x32b_x8(at, v8);
                             }
                         tc::wait_st();
                     }
+                    named_bar_sync(2 + grp, 128);  // the new maxima are visible, red is free
                 }
 
                 // with one P' buffer: the last tile's products have read it
                 if (NPB == 1 && gt >= 1) wait(bar_odone, gt - 1);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint64_t inv2 = pack2(kc[j].w, kc[j].w), zr2 = pack2(zr[j], zr[j]);
-                    const uint32_t pt = sPT + (gt % NPB) * C::PB_BYTES + 2 * j * C::PT_BYTES;
+                    const uint64_t inv2 = pack2(inv[j], inv[j]), zr2 = pack2(zr[j], zr[j]);
+                    const uint32_t pt = sPT + (gt % NPB) * C::PB_BYTES + j * C::PT_BYTES;
 #pragma unroll
                     for (int i0 = 0; i0 < HR; i0 += 8) {
-                        uint32_t hi[4], lo[4];
+                        uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int i = i0 / 2 + k;
@@ -741,18 +777,13 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                             l2[i] = fma2(x2, inv2, l2[i]);
                             z2[i] = fma2(x2, zr2, z2[i]);
                             const __half2 hv = __floats2half2_rn(x, y);
-                            const float2 r = __half22float2(hv);
-                            const __half2 lv = __floats2half2_rn(x - r.x, y - r.y);
-                            hi[k] = *reinterpret_cast<const uint32_t *>(&hv);
-                            lo[k] = *reinterpret_cast<const uint32_t *>(&lv);
+                            w[k] = *reinterpret_cast<const uint32_t *>(&hv);
                         }
                         const int chunk = (r0 + i0) / 8;
                         const uint32_t phys = C::PT_ROW == 128 ? (uint32_t)(chunk ^ (kt & 7))
                                               : C::PT_ROW == 64 ? (uint32_t)(chunk ^ ((kt >> 1) & 3))
                                                                 : (uint32_t)(chunk ^ ((kt >> 2) & 1));
-                        const uint32_t at = pt + (uint32_t)kt * C::PT_ROW + (phys << 4);
-                        st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        st_shared_v4(at + C::PT_BYTES, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                        st_shared_v4(pt + (uint32_t)kt * C::PT_ROW + (phys << 4), make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
                 fence_proxy_async_smem();
@@ -761,12 +792,14 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 if (lane == 0) mbar_arrive(bar_pfull + 8 * (gt % NPB));
             }
 
+            const int cur_b = b, cur_h = h, n_done = n;
+            have = walk.next(p.c, b, h, t0, n);
             // The next part's queries, while the last P.V runs: the last S of this part
             // was read above, so every S that used the query buffer is complete.
-            if (have_next) f_next = stage_q(nb, nh, part + 1) * p.scale_log2;
+            if (have) f = stage_q(b, h, part + 1) * p.scale_log2;
 
             // ---- the part's result: this thread owns tensor-memory lane kt of every O block
-            const int g_last = g + n - 1;
+            const int g_last = g + n_done - 1;
 #pragma unroll
             for (int i = 0; i < HR / 2; ++i) {
                 float l[2], z[2];
@@ -780,8 +813,9 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                         z[k] += __shfl_xor_sync(0xffffffffu, z[k], o);
                     }
                     if (lane == 0) {
-                        red[NR * q4 + r0 + 2 * i + k] = l[k];
-                        red[4 * NR + NR * q4 + r0 + 2 * i + k] = z[k];
+                        const uint32_t at = s_red + (NR * q4 + r0 + 2 * i + k) * 4;
+                        st_shared_f32(at, l[k]);
+                        st_shared_f32(at + 16 * NR, z[k]);
                     }
                 }
             }
@@ -789,15 +823,19 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             wait(bar_odone + 8 * (g_last % NPB), g_last / NPB);
             __syncwarp();
             tc::fence_after_sync();
-            const int64_t seg = (int64_t)blockIdx.x + (int64_t)b * p.c.n_kv_heads + h;
+            const int64_t seg = (int64_t)blockIdx.x + (int64_t)cur_b * p.c.n_kv_heads + cur_h;
 #pragma unroll
             for (int j = 0; j < HR / 8; ++j) {
                 float l8[8], z8[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float *rl = red + r0 + 8 * j + i, *rz = rl + 4 * NR;
-                    l8[i] = (rl[0] + rl[NR]) + (rl[2 * NR] + rl[3 * NR]);
-                    z8[i] = (rz[0] + rz[NR]) + (rz[2 * NR] + rz[3 * NR]);
+                    const uint32_t x = s_red + (r0 + 8 * j + i) * 4;
+                    const auto total = [&](uint32_t at) {
+                        return (ld_shared_f32(at) + ld_shared_f32(at + 4 * NR)) +
+                               (ld_shared_f32(at + 8 * NR) + ld_shared_f32(at + 12 * NR));
+                    };
+                    l8[i] = total(x);
+                    z8[i] = total(x + 16 * NR);
                 }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
@@ -817,19 +855,13 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 for (int i = 0; i < 8; ++i) {
                     const int r = r0 + 8 * j + i;
                     if (r < p.rows && kt == r)
-                        p.lse_part[seg * p.rows + r] = l8[i] == 0.f ? -CUDART_INF_F : lg2(l8[i]) - nm[8 * j + i];
+                        p.lse_part[seg * p.rows + r] = l8[i] == 0.f ? -CUDART_INF_F : lg2(l8[i]) - ld_shared_f32(nm + 4 * (8 * j + i));
                 }
             }
             // O has been read (wait_ld) before this warp's next pfull arrival, which gates the next part's first P.V
             tc::fence_before_sync();
-            g += n;
+            g += n_done;
             ++part;
-            f = f_next;
-            have = have_next;
-            b = nb;
-            h = nh;
-            t0 = nt0;
-            n = nn;
         }
     }
 
