@@ -388,7 +388,8 @@ size_t wm_workspace_size(int32_t op, int32_t batch, int32_t n_kv_heads, int32_t 
  *       data  [n_pages][n_kv_heads][page_size / 64][record]; page_size a
  *       multiple of 64; block_table [batch][max_pages] int32 as for wm_kv
  *   seq_lens [batch] int64: number of valid positions of each sequence.
- * data must be 16-byte aligned.  No initial contents are needed: positions at or
+ * A sequence holds at most INT32_MAX - 512 positions (n_cap, or max_pages *
+ * page_size; WM_ERR_UNSUPPORTED otherwise).  data must be 16-byte aligned.  No initial contents are needed: positions at or
  * past seq_lens[b] are never used, whatever their bytes.  A page that an append
  * writes must belong to one sequence.
  */

@@ -102,14 +102,14 @@ struct KvqCfg {
     static constexpr int NST = FIT > 8 ? 8 : FIT;
     static_assert(NST >= 2, "stages");
     static constexpr int CONST_OFF = ST_OFF + NST * STAGE;        // float4 [4][128], float [4][128]
-    static constexpr int RED_OFF = CONST_OFF + CONST_BYTES;       // float [2][4][NR]
+    static constexpr int RED_OFF = CONST_OFF + CONST_BYTES;       // float [2][NR][4]: per row and lane quadrant
     static constexpr int ZQ_OFF = RED_OFF + RED_BYTES;            // float [2][NR]: sums of a part's queries
     static constexpr int NM_OFF = ZQ_OFF + ROW_BYTES;             // float [2][NR]: minus (running maximum - kKvqOff)
     static constexpr int FLAG_OFF = NM_OFF + ROW_BYTES;           // int [64]: [0] abort, [8 + w] scratch
     static constexpr int BAR_OFF = FLAG_OFF + 256;
     static constexpr int NBAR = 2 * NST + 8 + 8 + 1 + 1 + 2 + 2 + 1 + 2;
     static_assert(NBAR * 8 <= 512, "barriers");
-    static constexpr int WARP_OFF = BAR_OFF + 512;                // int64 [32] + int4 of the schedule
+    static constexpr int WARP_OFF = BAR_OFF + 512;                // int [32] + KvqRun of the schedule
     static constexpr int TPTR_OFF = WARP_OFF + 32 * 8 + 16;
     static constexpr int TOTAL = ST_OFF + NST * STAGE + TAIL + 1024;
     static_assert(TPTR_OFF + 16 <= TOTAL - 1024 && TOTAL <= 227 * 1024, "shared memory");
@@ -181,6 +181,10 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
 }
 
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+    const uint4 v = ld_shared_v4(addr);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
 // Two pairs of fp32.
 __device__ __forceinline__ ulonglong2 ld_shared_pairs(uint32_t addr) {
     ulonglong2 v;
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     const uint32_t sbase = (raw + 1023u) & ~1023u;
     uint8_t *gb = smem_raw + (sbase - raw);
     const uint32_t sQ = sbase + C::Q_OFF, sPT = sbase + C::PT_OFF, sST = sbase + C::ST_OFF;
-    const uint32_t s_red = sbase + C::RED_OFF;              // float [2][4][NR]
+    const uint32_t s_red = sbase + C::RED_OFF;              // float [2][NR][4]
     const uint32_t s_zq = sbase + C::ZQ_OFF;                // float [2][NR]
     const uint32_t s_nm = sbase + C::NM_OFF;                // float [2][NR]
     const uint32_t s_const = sbase + C::CONST_OFF;          // float4 [4][128]
@@ -315,15 +319,17 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 
     pdl_wait();
     pdl_launch_dependents();
-    const int4 start = kvq_schedule(p, reinterpret_cast<int64_t *>(gb + C::WARP_OFF),
-                                    reinterpret_cast<int4 *>(gb + C::WARP_OFF + 32 * 8));
-    const int n_all = start.w;
+    const KvqRun run = p.c.batch <= kKvqWarpBatch
+                           ? kvq_schedule_warp(p, blockIdx.x == 0 && warp == 3)
+                           : kvq_schedule_block(p, reinterpret_cast<int *>(gb + C::WARP_OFF),
+                                                reinterpret_cast<KvqRun *>(gb + C::WARP_OFF + 32 * 4));
+    const int n_all = run.n;
     if (n_all <= 0) {
         if (warp == 1) tc::tmem_dealloc(tmem, 512);
         return;
     }
     KvqWalk walk;
-    walk.init(start);
+    walk.init(run);
 
     // Bounded wait for a barrier's phase; false once the pipeline is given up.
     const auto wait = [&](uint32_t bar, int phase) -> bool {
@@ -337,26 +343,27 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
         // lane looking up each page in turn held 64-position pages at a third of HBM's rate).
         const uint64_t policy = l2_policy_evict_first();
         const int rp = p.c.recs_per_page;
-        int b = 0, h = 0, t0 = 0, n = 0, g = 0, issued = 0;
+        int g = 0, issued = 0;
         bool stop = false;
-        while (!stop && walk.next(p.c, b, h, t0, n)) {
-            const int64_t len = kvq_len(p.c, b);
-            const int blk0 = (TK / kRecKeys) * t0;  // records of the part (capacity is below 2^31 positions)
-            const int blk1 = (int)min((int64_t)blk0 + (TK / kRecKeys) * (int64_t)n, (len + kRecKeys - 1) / kRecKeys);
+        KvqPart q;
+        while (!stop && walk.next(p.c, q)) {
+            const int n = q.n;
+            const int blk0 = (TK / kRecKeys) * q.t0;  // records of the part (capacity is below 2^31 positions)
+            const int blk1 = min(blk0 + (TK / kRecKeys) * n, (q.len + kRecKeys - 1) / kRecKeys);
             const auto record = [&](int blk) -> const uint8_t * {
                 if (blk >= blk1) return nullptr;
-                int64_t page = b;
+                int64_t page = q.b;
                 int within = blk;
                 if (p.c.block_table) {
                     const int e = blk / rp;
                     within = blk - e * rp;
-                    page = p.c.block_table[(int64_t)b * p.c.max_pages + e];
+                    page = p.c.block_table[(int64_t)q.b * p.c.max_pages + e];
                     if (page < 0 || page >= p.c.n_pages) {
                         kvq_report(p.err, WM_DEVERR_BAD_PAGE);
                         page = 0;
                     }
                 }
-                return p.c.data + ((page * p.c.n_kv_heads + h) * rp + within) * (int64_t)C::REC;
+                return p.c.data + ((page * p.c.n_kv_heads + q.h) * rp + within) * (int64_t)C::REC;
             };
             const uint8_t *cur = record(blk0 + lane);
             for (int i0 = 0; !stop && i0 < 2 * n; i0 += 16) {
@@ -389,11 +396,12 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
         if (elect_one()) {
             constexpr uint32_t id_s = idesc_f16(NR, 0);
             const uint64_t q_desc = tc::smem_desc(sQ, 16, 1024, tc::SWIZZLE_128B);
-            int xb, xh, xt, n = 0, part = 0;
+            KvqPart q;
+            int part = 0;
             bool ok = true;
-            for (int g = 0; ok && walk.next(p.c, xb, xh, xt, n); g += n, ++part) {
+            for (int g = 0; ok && walk.next(p.c, q); g += q.n, ++part) {
                 ok = wait(bar_qfull, part);
-                for (int t = 0; ok && t < n; ++t) {
+                for (int t = 0; ok && t < q.n; ++t) {
                     const int gt = g + t;
                     if (gt >= 1) ok = wait(bar_sfree, gt - 1);
                     // with two P' buffers: S of a tile also says that its buffer is free
@@ -430,10 +438,10 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
         if (elect_one()) {
             constexpr uint32_t id_pv = idesc_f16(NR, 1);
             const uint64_t p_desc = tc::smem_desc(sPT, C::PT_BYTES, C::PT_ATOM, C::PT_SWIZZLE);
-            int xb, xh, xt, n = 0;
+            KvqPart q;
             bool ok = true;
-            for (int g = 0; ok && walk.next(p.c, xb, xh, xt, n); g += n) {
-                for (int t = 0; ok && t < n; ++t) {
+            for (int g = 0; ok && walk.next(p.c, q); g += q.n) {
+                for (int t = 0; ok && t < q.n; ++t) {
                     const int gt = g + t, buf = gt % NPB;
                     ok = wait(bar_pfull + 8 * buf, gt / NPB);
 #pragma unroll
@@ -639,14 +647,15 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             return __uint_as_float((uint32_t)(127 + ex) << 23);
         };
 
-        int b = 0, h = 0, t0 = 0, n = 0, g = 0, part = 0;
-        bool have = walk.next(p.c, b, h, t0, n);
-        float f = have ? stage_q(b, h, 0) * p.scale_log2 : 0.f;
+        KvqPart q;
+        int g = 0, part = 0;
+        bool have = walk.next(p.c, q);
+        float f = have ? stage_q(q.b, q.h, 0) * p.scale_log2 : 0.f;
         while (have) {
             // positions fit 32 bits (the capacity does)
-            const int len = (int)kvq_len(p.c, b);
-            const int key_first = t0 * TK, key_end = (int)min((int64_t)(t0 + n) * TK, (int64_t)len);
-            const int qpos0 = len - p.n_q;
+            const int n = q.n, key_first = q.t0 * TK;
+            const int key_end = (int)min((int64_t)(q.t0 + n) * TK, (int64_t)q.len);
+            const int qpos0 = q.len - p.n_q;
             const uint32_t zq = s_zq + ((part & 1) * NR + r0) * 4, nm = s_nm + ((part & 1) * NR + r0) * 4;
 
             uint64_t l2[HR / 2], z2[HR / 2];  // sums of P' / s_V and P' z_V / s_V, two rows each
@@ -715,14 +724,13 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 #pragma unroll
                     for (int i = 0; i < HR; ++i) {
                         const float mx = warp_max_f(fmaxf(s[0][i], s[1][i]));
-                        if (lane == 0) st_shared_f32(s_red + (NR * q4 + r0 + i) * 4, mx);
+                        if (lane == 0) st_shared_f32(s_red + (4 * (r0 + i) + q4) * 4, mx);
                     }
                     named_bar_sync(2 + grp, 128);
                     // by how much row i's maximum goes up
                     const auto up = [&](int i) -> float {
-                        const uint32_t x = s_red + (r0 + i) * 4;
-                        const float mx = fmaxf(fmaxf(ld_shared_f32(x), ld_shared_f32(x + 4 * NR)),
-                                               fmaxf(ld_shared_f32(x + 8 * NR), ld_shared_f32(x + 12 * NR))) - kKvqOff;
+                        const float4 x = ld_shared_f4(s_red + 16 * (r0 + i));
+                        const float mx = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - kKvqOff;
                         return t > 0 ? fmaxf(mx, 0.f) : mx == -CUDART_INF_F ? 0.f : mx;
                     };
 #pragma unroll
@@ -792,50 +800,47 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 if (lane == 0) mbar_arrive(bar_pfull + 8 * (gt % NPB));
             }
 
-            const int cur_b = b, cur_h = h, n_done = n;
-            have = walk.next(p.c, b, h, t0, n);
+            const int64_t seg = (int64_t)blockIdx.x + (int64_t)q.b * p.c.n_kv_heads + q.h;
+            have = walk.next(p.c, q);
             // The next part's queries, while the last P.V runs: the last S of this part
             // was read above, so every S that used the query buffer is complete.
-            if (have) f = stage_q(b, h, part + 1) * p.scale_log2;
+            if (have) f = stage_q(q.b, q.h, part + 1) * p.scale_log2;
 
             // ---- the part's result: this thread owns tensor-memory lane kt of every O block
-            const int g_last = g + n_done - 1;
+            const int g_last = g + n - 1;
+            // Sums over the lanes: halve the values and the lanes that hold them at each step
+            // (HR = 16: 31 shuffles for 32 sums), until lane i holds sum number i.
+            float y[2 * HR];
 #pragma unroll
             for (int i = 0; i < HR / 2; ++i) {
-                float l[2], z[2];
-                unpack2(l2[i], l[0], l[1]);
-                unpack2(z2[i], z[0], z[1]);
+                unpack2(l2[i], y[2 * i], y[2 * i + 1]);
+                unpack2(z2[i], y[HR + 2 * i], y[HR + 2 * i + 1]);
+            }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+            for (int o = HR; o >= 1; o >>= 1) {
+                const bool up = lane & o;
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) {
-                        l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
-                        z[k] += __shfl_xor_sync(0xffffffffu, z[k], o);
-                    }
-                    if (lane == 0) {
-                        const uint32_t at = s_red + (NR * q4 + r0 + 2 * i + k) * 4;
-                        st_shared_f32(at, l[k]);
-                        st_shared_f32(at + 16 * NR, z[k]);
-                    }
+                for (int i = 0; i < o; ++i) {
+                    const float send = up ? y[i] : y[i + o], keep = up ? y[i + o] : y[i];
+                    y[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
                 }
             }
+            if (HR == 8) y[0] += __shfl_xor_sync(0xffffffffu, y[0], 16);
+            if (lane < 2 * HR)  // sums of l, then of z
+                st_shared_f32(s_red + (lane / HR) * 16 * NR + (4 * (r0 + lane % HR) + q4) * 4, y[0]);
             named_bar_sync(2 + grp, 128);
             wait(bar_odone + 8 * (g_last % NPB), g_last / NPB);
             __syncwarp();
             tc::fence_after_sync();
-            const int64_t seg = (int64_t)blockIdx.x + (int64_t)cur_b * p.c.n_kv_heads + cur_h;
 #pragma unroll
             for (int j = 0; j < HR / 8; ++j) {
                 float l8[8], z8[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint32_t x = s_red + (r0 + 8 * j + i) * 4;
-                    const auto total = [&](uint32_t at) {
-                        return (ld_shared_f32(at) + ld_shared_f32(at + 4 * NR)) +
-                               (ld_shared_f32(at + 8 * NR) + ld_shared_f32(at + 12 * NR));
-                    };
-                    l8[i] = total(x);
-                    z8[i] = total(x + 16 * NR);
+                    const uint32_t at = s_red + 16 * (r0 + 8 * j + i);
+                    const float4 x = ld_shared_f4(at), z = ld_shared_f4(at + 16 * NR);
+                    l8[i] = (x.x + x.y) + (x.z + x.w);
+                    z8[i] = (z.x + z.y) + (z.z + z.w);
                 }
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             }
             // O has been read (wait_ld) before this warp's next pfull arrival, which gates the next part's first P.V
             tc::fence_before_sync();
-            g += n_done;
+            g += n;
             ++part;
         }
     }

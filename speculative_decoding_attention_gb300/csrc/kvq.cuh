@@ -74,7 +74,7 @@ struct KvqAttnParams {
     const void *q;       // [B][n_q][Hq][D] bf16
     int32_t n_q, n_q_heads, group, rows;
     float scale_log2;    // scale * log2(e)
-    int64_t *sched;      // [batch + 2]: tiles per CTA, then the tile prefix [batch + 1] (written by CTA 0)
+    int32_t *sched;      // [batch + 2]: tiles per CTA, then the tile prefix [batch + 1] (written by CTA 0)
     float *o_part;       // [n_cta + units - 1][rows][D]: each part normalised by its own sum
     float *lse_part;     // [n_cta + units - 1][rows], log2 units; -inf marks a part without a visible key
     void *out;
@@ -96,51 +96,100 @@ __device__ __forceinline__ int kvq_tiles(const KvqView &c, int b) {
 // lengths.  The part of CTA c in unit u has index c + u: along the tiles each
 // next part starts at a new CTA, a new unit or both, so the indexes rise and stay
 // below n_cta + units - 1.  Every CTA works this out for itself from the
-// lengths (one load per sequence, spread over the block, and one block-wide
-// scan, about a microsecond) -- a launch of its own would cost more.  CTA 0 also
-// leaves the chunk and the prefix for the merge.  Block-wide; returns
-// (sequence, KV head, first tile in the unit, tiles), 0 tiles for no work.
-__device__ __forceinline__ int4 kvq_schedule(const KvqAttnParams &p, int64_t *s_warp, int4 *s_start) {
+// lengths; a launch of its own would cost more.  CTA 0 also leaves the chunk and the
+// prefix for the merge.  Tile counts fit 32 bits (at most 2^30 per call).
+struct KvqRun {
+    int b, h, t, n;  // sequence, KV head, first tile in the unit, tiles (0: no work)
+    int len;         // positions of sequence b
+};
+
+// Run of `chunk` tiles at t0, found in sequences lo .. hi - 1 (acc tiles of one head before lo).
+__device__ __forceinline__ KvqRun kvq_find(const KvqView &c, int lo, int hi, int acc, int t0, int n) {
+    KvqRun r = {0, 0, 0, 0, 0};
+    for (int b = lo; b < hi; ++b) {
+        const int len = (int)kvq_len(c, b), nt = (len + kKvqTile - 1) / kKvqTile;
+        if ((acc + nt) * c.n_kv_heads > t0) {
+            const int within = t0 - acc * c.n_kv_heads;
+            r.b = b;
+            r.h = within / nt;
+            r.t = within - r.h * nt;
+            r.n = n;
+            r.len = len;
+            break;
+        }
+        acc += nt;
+    }
+    return r;
+}
+
+__device__ __forceinline__ int kvq_inclusive(int x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+constexpr int kKvqWarpBatch = 256;  // sequences up to which every warp finds the run by itself
+
+// By one warp (batch <= kKvqWarpBatch), with no barrier; `leave`: this warp writes the schedule.
+__device__ __forceinline__ KvqRun kvq_schedule_warp(const KvqAttnParams &p, bool leave) {
+    const KvqView &c = p.c;
+    const int lane = threadIdx.x & 31;
+    const int per = (c.batch + 31) / 32;
+    const int lo = min(c.batch, lane * per), hi = min(c.batch, lo + per);
+    int mine = 0;
+    for (int b = lo; b < hi; ++b) mine += kvq_tiles(c, b);
+    const int incl = kvq_inclusive(mine, lane);
+    const int all = __shfl_sync(0xffffffffu, incl, 31), total = all * c.n_kv_heads;
+    const int chunk = total > 0 ? (total + (int)gridDim.x - 1) / (int)gridDim.x : 1;
+    if (leave) {
+        int acc = incl - mine;
+        if (lane == 0) {
+            p.sched[0] = chunk;
+            p.sched[1 + c.batch] = all;
+        }
+        for (int b = lo; b < hi; ++b) {
+            p.sched[1 + b] = acc;
+            acc += kvq_tiles(c, b);
+            if (c.seq_lens[b] != kvq_len(c, b)) kvq_report(p.err, WM_DEVERR_BAD_LENGTH);
+        }
+    }
+    const int64_t t0 = (int64_t)blockIdx.x * chunk;
+    KvqRun r = {0, 0, 0, 0, 0};
+    if (t0 >= total) return r;
+    const bool has = (incl - mine) * c.n_kv_heads <= t0 && t0 < incl * c.n_kv_heads;
+    if (has) r = kvq_find(c, lo, hi, incl - mine, (int)t0, min(chunk, total - (int)t0));
+    const int src = __ffs(__ballot_sync(0xffffffffu, has)) - 1;
+    r.b = __shfl_sync(0xffffffffu, r.b, src);
+    r.h = __shfl_sync(0xffffffffu, r.h, src);
+    r.t = __shfl_sync(0xffffffffu, r.t, src);
+    r.n = __shfl_sync(0xffffffffu, r.n, src);
+    r.len = __shfl_sync(0xffffffffu, r.len, src);
+    return r;
+}
+
+// By the whole block, for larger batches.
+__device__ __forceinline__ KvqRun kvq_schedule_block(const KvqAttnParams &p, int *s_warp, KvqRun *s_run) {
     const KvqView &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
     const int per = (c.batch + (int)blockDim.x - 1) / (int)blockDim.x;
     const int lo = min(c.batch, tid * per), hi = min(c.batch, lo + per);
-    int64_t mine = 0;
-    for (int b = lo; b < hi; ++b) {
-        if (blockIdx.x == 0 && c.seq_lens[b] != kvq_len(c, b)) kvq_report(p.err, WM_DEVERR_BAD_LENGTH);
-        mine += kvq_tiles(c, b);
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
+    int mine = 0;
+    for (int b = lo; b < hi; ++b) mine += kvq_tiles(c, b);
+    const int incl = kvq_inclusive(mine, lane);
     if (lane == 31) s_warp[warp] = incl;
-    if (tid == 0) *s_start = make_int4(0, 0, 0, 0);
+    if (tid == 0) *s_run = KvqRun{0, 0, 0, 0, 0};
     __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < n_warps; ++w) {
-        if (w < warp) before += s_warp[w];
-        all += s_warp[w];
-    }
-    int64_t acc = before + incl - mine;  // tiles (of one KV head) before sequence lo
-    const int64_t total = all * c.n_kv_heads;
-    const int64_t chunk = total > 0 ? (total + gridDim.x - 1) / gridDim.x : 1;
+    const int w = kvq_inclusive(lane < n_warps ? s_warp[lane] : 0, lane);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0)), all = __shfl_sync(0xffffffffu, w, 31);
+    int acc = (warp > 0 ? before : 0) + incl - mine;  // tiles of one head before sequence lo
+    const int total = all * c.n_kv_heads;
+    const int chunk = total > 0 ? (total + (int)gridDim.x - 1) / (int)gridDim.x : 1;
     const int64_t t0 = (int64_t)blockIdx.x * chunk;
-    if (t0 < total && acc * c.n_kv_heads <= t0 && t0 < (acc + mine) * c.n_kv_heads) {
-        int64_t a = acc;
-        for (int b = lo; b < hi; ++b) {
-            const int nt = kvq_tiles(c, b);
-            if ((a + nt) * c.n_kv_heads > t0) {
-                const int64_t within = t0 - a * c.n_kv_heads;
-                const int h = (int)(within / nt);
-                *s_start = make_int4(b, h, (int)(within - (int64_t)h * nt), (int)min(chunk, total - t0));
-                break;
-            }
-            a += nt;
-        }
-    }
+    if (t0 < total && acc * c.n_kv_heads <= t0 && t0 < (acc + mine) * c.n_kv_heads)
+        *s_run = kvq_find(c, lo, hi, acc, (int)t0, min(chunk, total - (int)t0));
     if (blockIdx.x == 0) {
         if (tid == 0) {
             p.sched[0] = chunk;
@@ -149,35 +198,41 @@ __device__ __forceinline__ int4 kvq_schedule(const KvqAttnParams &p, int64_t *s_
         for (int b = lo; b < hi; ++b) {
             p.sched[1 + b] = acc;
             acc += kvq_tiles(c, b);
+            if (c.seq_lens[b] != kvq_len(c, b)) kvq_report(p.err, WM_DEVERR_BAD_LENGTH);
         }
     }
     __syncthreads();
-    return *s_start;
+    return *s_run;
 }
 
-// Walks the parts of one CTA's run: tiles [t0, t0 + n) of unit (sb, sh).
+// Walks the parts of one CTA's run: tiles [t0, t0 + n) of unit (b, h), b of length len.
+struct KvqPart {
+    int b, h, t0, n, len;
+};
 struct KvqWalk {
-    int b, h, t_off, left;
-    __device__ __forceinline__ void init(int4 st) {
-        b = st.x;
-        h = st.y;
-        t_off = st.z;
-        left = st.w;
+    int b, h, t_off, left, len;
+    __device__ __forceinline__ void init(const KvqRun &r) {
+        b = r.b;
+        h = r.h;
+        t_off = r.t;
+        left = r.n;
+        len = r.len;
     }
-    __device__ __forceinline__ bool next(const KvqView &c, int &sb, int &sh, int &t0, int &n) {
+    __device__ __forceinline__ bool next(const KvqView &c, KvqPart &q) {
         while (left > 0 && b < c.batch) {
-            const int nt = kvq_tiles(c, b);
+            const int nt = (len + kKvqTile - 1) / kKvqTile;
             if (nt <= 0 || h == c.n_kv_heads) {  // no keys, or the sequence's last head is done
-                ++b;
+                if (++b < c.batch) len = (int)kvq_len(c, b);
                 h = 0;
                 t_off = 0;
                 continue;
             }
-            sb = b;
-            sh = h;
-            t0 = t_off;
-            n = min(nt - t_off, left);
-            left -= n;
+            q.b = b;
+            q.h = h;
+            q.t0 = t_off;
+            q.n = min(nt - t_off, left);
+            q.len = len;
+            left -= q.n;
             t_off = 0;
             ++h;
             return true;

@@ -24,20 +24,19 @@ __global__ void __launch_bounds__(kColThreads *kPartGroups) kvq_merge_kernel(con
     pdl_wait();
     pdl_launch_dependents();
     const int D = p.c.head_dim;
-    const int64_t r = blockIdx.x;
+    const int r = blockIdx.x;
     const int ct = threadIdx.x % kColThreads, pg = threadIdx.x / kColThreads;
     const int col = ((int)blockIdx.y * kColThreads + ct) * 4;
-    const int64_t per_b = (int64_t)p.n_q * p.n_q_heads;
-    const int b = (int)(r / per_b);
-    const int rem = (int)(r - b * per_b), qi = rem / p.n_q_heads, head = rem - qi * p.n_q_heads;
+    const int per_b = p.n_q * p.n_q_heads;
+    const int b = r / per_b, rem = r - b * per_b, qi = rem / p.n_q_heads, head = rem - qi * p.n_q_heads;
     const int h = head / p.group, ru = qi * p.group + head - h * p.group;
-    const int64_t chunk = p.sched[0], before = p.sched[1 + b], nt = p.sched[2 + b] - before;
+    const int chunk = p.sched[0], before = p.sched[1 + b], nt = p.sched[2 + b] - before;
     int64_t s_first = 0;
     int n_parts = 0;
     if (nt > 0) {
-        const int64_t first = before * p.c.n_kv_heads + h * nt;
-        const int64_t c0 = first / chunk, c1 = (first + nt - 1) / chunk;
-        n_parts = (int)(c1 - c0 + 1);
+        const int first = before * p.c.n_kv_heads + h * nt;
+        const int c0 = first / chunk, c1 = (first + nt - 1) / chunk;
+        n_parts = c1 - c0 + 1;
         s_first = c0 + (int64_t)b * p.c.n_kv_heads + h;
     }
     const float *ls = p.lse_part + s_first * p.rows + ru;
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(kColThreads *kPartGroups) kvq_merge_kernel(con
     uint2 pk;
     pk.x = *reinterpret_cast<const uint32_t *>(&lo);
     pk.y = *reinterpret_cast<const uint32_t *>(&hi);
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + r * D + col) = pk;
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + (int64_t)r * D + col) = pk;
     if (blockIdx.y == 0 && ct == 0 && p.lse) p.lse[r] = zt == 0.f ? -CUDART_INF_F : (mt + lg2(zt)) * kLn2;
 }
 

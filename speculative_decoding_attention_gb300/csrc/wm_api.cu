@@ -362,6 +362,9 @@ int64_t mem_base_of(const wm_ring *ring) {
 
 // ---- 4-bit cache
 
+// positions of a sequence: a whole tile past any of them is still a 32-bit index
+constexpr int64_t kKvqMaxPositions = INT32_MAX - 2 * kKvqTile;
+
 wm_status kvq_check(const wm_kvq *kv) {
     if (!kv || !kv->data || !kv->seq_lens || kv->batch <= 0 || kv->n_kv_heads <= 0) return WM_ERR_INVALID_ARG;
     if (!head_dim_ok(kv->head_dim)) return WM_ERR_UNSUPPORTED;
@@ -370,11 +373,11 @@ wm_status kvq_check(const wm_kvq *kv) {
         if (kv->page_size <= 0 || kv->max_pages <= 0 || kv->n_pages <= 0 || !aligned(kv->block_table, 4))
             return WM_ERR_INVALID_ARG;
         if (kv->page_size % kRecKeys || kv->n_pages > INT32_MAX ||
-            (int64_t)kv->max_pages * kv->page_size > INT32_MAX)
+            (int64_t)kv->max_pages * kv->page_size > kKvqMaxPositions)
             return WM_ERR_UNSUPPORTED;
     } else {
         if (kv->n_cap <= 0) return WM_ERR_INVALID_ARG;
-        if (kv->n_cap % kRecKeys || kv->n_cap > INT32_MAX) return WM_ERR_UNSUPPORTED;
+        if (kv->n_cap % kRecKeys || kv->n_cap > kKvqMaxPositions) return WM_ERR_UNSUPPORTED;
     }
     if ((int64_t)kv->batch * kv->n_kv_heads > kMaxUnits) return WM_ERR_UNSUPPORTED;
     return WM_OK;
@@ -406,7 +409,7 @@ KvqLayout kvq_layout(int n_cta, int64_t units, int rows, int head_dim, int batch
     KvqLayout l;
     l.lse = up(n_part * rows * head_dim * sizeof(float));
     l.sched = l.lse + up(n_part * rows * sizeof(float));
-    l.total = l.sched + ((size_t)batch + 2) * sizeof(int64_t);
+    l.total = l.sched + ((size_t)batch + 2) * sizeof(int32_t);
     return l;
 }
 // One CTA per SM.
@@ -875,7 +878,7 @@ wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.o_part = reinterpret_cast<float *>(w);
     p.lse_part = reinterpret_cast<float *>(w + l.lse);
-    p.sched = reinterpret_cast<int64_t *>(w + l.sched);
+    p.sched = reinterpret_cast<int32_t *>(w + l.sched);
     p.out = out;
     p.lse = lse;
     p.err = device_error_ptr();
