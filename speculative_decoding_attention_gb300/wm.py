@@ -481,35 +481,34 @@ def lse_merge(o_parts: torch.Tensor, lse_parts: torch.Tensor, out=None, lse=None
     return out, lse
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _arg(t: torch.Tensor, dtype, shape: tuple, device: int, what: str) -> int:
     """Address of an argument of the given type and shape on the current device."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{what} must be {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous CUDA tensor")
-    if t.get_device() != device:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device or device < 0 or not t.is_contiguous():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous CUDA tensor")
         raise ValueError(f"{what} must be on the current device (cuda:{device}), is on {t.device}")
     return t.data_ptr()
 
 
-def _new_on(stream, shape: tuple, dtype, device: int) -> torch.Tensor:
+def _new_on(stream, shape: tuple, dtype, device: int, new=None) -> torch.Tensor:
     """A buffer that belongs to the stream the call runs on, so that its memory
     is handed on in that stream's order."""
+    new = _new_out if new is None else new
     if stream is None:
-        return _new_out(shape, dtype, device)
+        return new(shape, dtype, device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     with torch.cuda.stream(stream):
-        return _new_out(shape, dtype, device)
+        return new(shape, dtype, device)
 
 
-def _new_int(stream, shape: tuple, dtype, device: int) -> torch.Tensor:
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _new_int(shape: tuple, dtype, device: int) -> torch.Tensor:
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 KVQ_RECORD_KEYS = 64  # positions per record
@@ -570,9 +569,9 @@ class KVQCache:
 
 
 def _kvq_device(cache: KVQCache) -> int:
-    device = torch.cuda.current_device()
-    if cache.device != device:
-        raise ValueError(f"the cache must be on the current device (cuda:{device}), is on cuda:{cache.device}")
+    device = cache.device
+    if device != _current_device():
+        raise ValueError(f"the cache must be on the current device (cuda:{_current_device()}), is on cuda:{device}")
     return device
 
 
@@ -584,9 +583,9 @@ def kvq_append(cache: KVQCache, k_new: torch.Tensor, v_new: torch.Tensor, stream
         raise ValueError(f"k_new must be [B, n, Hkv, D], got {tuple(k_new.shape)}")
     n = k_new.shape[1]
     shape = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
-    _check(load().wm_kvq_append(cache._ref, _arg(k_new, torch.bfloat16, shape, device, "k_new"),
-                                _arg(v_new, torch.bfloat16, shape, device, "v_new"), n, _stream(stream)),
-           "wm_kvq_append")
+    status = load().wm_kvq_append(cache._ref, _arg(k_new, torch.bfloat16, shape, device, "k_new"),
+                                  _arg(v_new, torch.bfloat16, shape, device, "v_new"), n, _stream(stream))
+    _check(status, "wm_kvq_append")
 
 
 def kvq_read(cache: KVQCache, n: int, k_out=None, v_out=None, stream=None):
@@ -597,8 +596,9 @@ def kvq_read(cache: KVQCache, n: int, k_out=None, v_out=None, stream=None):
         k_out = _new_on(stream, shape, torch.bfloat16, device)
     if v_out is None:
         v_out = _new_on(stream, shape, torch.bfloat16, device)
-    _check(load().wm_kvq_read(cache._ref, n, _arg(k_out, torch.bfloat16, shape, device, "k_out"),
-                              _arg(v_out, torch.bfloat16, shape, device, "v_out"), _stream(stream)), "wm_kvq_read")
+    status = load().wm_kvq_read(cache._ref, n, _arg(k_out, torch.bfloat16, shape, device, "k_out"),
+                                _arg(v_out, torch.bfloat16, shape, device, "v_out"), _stream(stream))
+    _check(status, "wm_kvq_read")
     return k_out, v_out
 
 
@@ -617,27 +617,31 @@ def kvq_workspace(cache: KVQCache, n_q_heads: int, n_q: int) -> torch.Tensor:
 
 def verify_attn_kvq(cache: KVQCache, q: torch.Tensor, scale: float, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [B, T, Hq, D] over a 4-bit cache (T = 1: single-token
-    decode); returns (out bf16, lse fp32)."""
+    decode); returns (out bf16, lse fp32).  Buffers that are not given are allocated."""
     device = _kvq_device(cache)
     if q.dim() != 4:
         raise ValueError(f"q must be [B, T, Hq, D], got {tuple(q.shape)}")
-    T, Hq = q.shape[1], q.shape[2]
-    shape = (cache.batch, T, Hq, cache.head_dim)
-    qp = _arg(q, torch.bfloat16, shape, device, "q")
+    _, T, Hq, _ = q.shape
+    B, D = cache.batch, cache.head_dim
+    qp = _arg(q, torch.bfloat16, (B, T, Hq, D), device, "q")
     if out is None:
-        out = _new_on(stream, shape, torch.bfloat16, device)
+        out = _new_on(stream, (B, T, Hq, D), torch.bfloat16, device)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, torch.bfloat16, (B, T, Hq, D), device, "out")
     if lse is None:
-        lse = _new_on(stream, shape[:3], torch.float32, device)
+        lse = _new_on(stream, (B, T, Hq), torch.float32, device)
+        lp = lse.data_ptr()
+    else:
+        lp = _arg(lse, torch.float32, (B, T, Hq), device, "lse")
     if workspace is None:
-        need = kvq_workspace_size(cache.batch, cache.n_kv_heads, Hq, T, cache.head_dim)
+        need = kvq_workspace_size(B, cache.n_kv_heads, Hq, T, D)
         workspace = _new_on(stream, (-(-need // 4),), torch.float32, device)
-    elif workspace.get_device() != device:
-        raise ValueError(f"workspace must be on the current device (cuda:{device}), is on {workspace.device}")
-    _check(load().wm_verify_attn_kvq(cache._ref, qp, T, Hq, float(scale),
-                                     _arg(out, torch.bfloat16, shape, device, "out"),
-                                     _arg(lse, torch.float32, shape[:3], device, "lse"), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream(stream)),
-           "wm_verify_attn_kvq")
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on the current device (cuda:{device})")
+    status = load().wm_verify_attn_kvq(cache._ref, qp, T, Hq, scale, op, lp, workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(status, "wm_verify_attn_kvq")
     return out, lse
 
 
@@ -650,31 +654,39 @@ def spec_accept(target_probs: torch.Tensor, draft_probs: torch.Tensor | None, dr
     (tokens [B, k + 1] int32, n_accepted [B] int32, new_len [B] int64); new_len --
     what ring_rollback takes -- is None without ``seq_lens`` [B] int64, the cache
     lengths with the k + 1 verified positions.  See wm_spec_accept in include/wm_api.h."""
-    device = torch.cuda.current_device()
+    device = _current_device()
     if target_probs.dim() != 3 or draft_tokens.dim() != 2:
         raise ValueError("target_probs must be [B, k + 1, V] and draft_tokens [B, k]")
     B, k = draft_tokens.shape
     V = target_probs.shape[2]
     f32, i32, i64 = torch.float32, torch.int32, torch.int64
-    pp = _arg(target_probs, f32, (B, k + 1, V), device, "target_probs")
-    qp = _arg(draft_probs, f32, (B, k, V), device, "draft_probs") if draft_probs is not None else None
-    xp = _arg(draft_tokens, i32, (B, k), device, "draft_tokens")
-    np_ = _arg(n_draft, i32, (B,), device, "n_draft") if n_draft is not None else None
-    sp = _arg(seq_lens, i64, (B,), device, "seq_lens") if seq_lens is not None else None
     if new_len is not None and seq_lens is None:
         raise ValueError("new_len needs seq_lens")
+    pp = _arg(target_probs, f32, (B, k + 1, V), device, "target_probs")
+    qp = None if draft_probs is None else _arg(draft_probs, f32, (B, k, V), device, "draft_probs")
+    xp = _arg(draft_tokens, i32, (B, k), device, "draft_tokens")
+    dp = None if n_draft is None else _arg(n_draft, i32, (B,), device, "n_draft")
+    ap = _arg(u_accept, f32, (B, k), device, "u_accept")
+    wp = _arg(u_sample, f32, (B,), device, "u_sample")
+    sp = None if seq_lens is None else _arg(seq_lens, i64, (B,), device, "seq_lens")
+    np = None
     if tokens is None:
-        tokens = _new_int(stream, (B, k + 1), i32, device)
+        tokens = _new_on(stream, (B, k + 1), i32, device, _new_int)
+        tp = tokens.data_ptr()
+    else:
+        tp = _arg(tokens, i32, (B, k + 1), device, "tokens")
     if n_accepted is None:
-        n_accepted = _new_int(stream, (B,), i32, device)
-    if new_len is None and seq_lens is not None:
-        new_len = _new_int(stream, (B,), i64, device)
-    _check(load().wm_spec_accept(pp, qp, xp, np_, _arg(u_accept, f32, (B, k), device, "u_accept"),
-                                 _arg(u_sample, f32, (B,), device, "u_sample"), sp, B, k, V,
-                                 _arg(tokens, i32, (B, k + 1), device, "tokens"),
-                                 _arg(n_accepted, i32, (B,), device, "n_accepted"),
-                                 _arg(new_len, i64, (B,), device, "new_len") if new_len is not None else None,
-                                 _stream(stream)), "wm_spec_accept")
+        n_accepted = _new_on(stream, (B,), i32, device, _new_int)
+        cp = n_accepted.data_ptr()
+    else:
+        cp = _arg(n_accepted, i32, (B,), device, "n_accepted")
+    if new_len is not None:
+        np = _arg(new_len, i64, (B,), device, "new_len")
+    elif seq_lens is not None:
+        new_len = _new_on(stream, (B,), i64, device, _new_int)
+        np = new_len.data_ptr()
+    status = load().wm_spec_accept(pp, qp, xp, dp, ap, wp, sp, B, k, V, tp, cp, np, _stream(stream))
+    _check(status, "wm_spec_accept")
     return tokens, n_accepted, new_len
 
 
