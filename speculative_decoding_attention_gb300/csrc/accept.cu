@@ -5,11 +5,11 @@
 // a = the accepted count.  One more token comes from r = max(p_a - q_a, 0) if
 // a < n, else r = p_n, by inversion: the least i with r_0 + .. + r_i > w sum(r).
 //
-// Exactness: the products u q are exact in 64 bits, and a difference p - q
-// with p > q is exact as a pair of floats (d = fl(p - q), e = (p - d) - q).
-// Sums run in such pairs (two-sum, about 48 bits) per lane and in doubles
-// above; the 64-bit units of this GPU are too few (about 2 FMA per SM and
-// clock) to add every entry in doubles: 128K entries on one SM would take 35 us.
+// Exactness: a product u q is compared as the pair (fl(u q), its error), and a
+// difference p - q with p > q is exact as a pair of floats (d = fl(p - q), e = (p - d) - q).
+// Every sum is such a pair (two-sum, about 48 bits), at every level: this GPU has 2 FP64
+// units per SM, on which one scan of a warp took 1000 clocks where a scan of
+// pairs takes 300.
 //
 // One cluster of CTAs per sequence: each CTA sums a run of the row, the totals
 // meet through distributed shared memory, and the CTA that holds the threshold
@@ -32,30 +32,53 @@ namespace cg = cooperative_groups;
 
 constexpr int kAcceptThreads = 512;
 constexpr int kAcceptWarps = kAcceptThreads / 32;
-constexpr int kLoads = 8;  // entries per lane whose loads are in flight together
+constexpr int kLoads = 4;  // entries per lane whose loads are in flight together
 
+// hi + lo, hi the nearest float.
 struct Pair {
     float hi = 0.f, lo = 0.f;
-    // + (d + e), d exact
+    // + (d + e), d exact; lo is left to grow
     __device__ __forceinline__ void add(float d, float e) {
         const float s = hi + d;
         const float bb = s - hi;
         lo += ((hi - (s - bb)) + (d - bb)) + e;
         hi = s;
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ bool positive() const { return hi > 0.f; }
 };
+
+// The same bits whichever operand comes first.
+__device__ __forceinline__ Pair operator+(const Pair &a, const Pair &b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    const float e = ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo);
+    Pair r;
+    r.hi = s + e;
+    r.lo = e - (r.hi - s);
+    return r;
+}
+
+__device__ __forceinline__ bool operator>(const Pair &a, const Pair &b) {
+    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+
+// u x, u a float
+__device__ __forceinline__ Pair times(float u, const Pair &x) {
+    const float h = u * x.hi, l = fmaf(u, x.hi, -h) + u * x.lo;
+    Pair r;
+    r.hi = h + l;
+    r.lo = l - (r.hi - h);
+    return r;
+}
+
+__device__ __forceinline__ Pair shfl(const Pair &x, int lane) {
+    return Pair{__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane)};
+}
 
 // Sum over the lanes of a warp, on every lane.
 __device__ __forceinline__ Pair warp_sum(Pair x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float d = __shfl_xor_sync(0xffffffffu, x.hi, o), e = __shfl_xor_sync(0xffffffffu, x.lo, o);
-        // the same operation on both sides, so that all lanes end with the same bits
-        const Pair a = x.hi >= d ? x : Pair{d, e}, b = x.hi >= d ? Pair{d, e} : x;
-        x = a;
-        x.add(b.hi, b.lo);
-    }
+    for (int o = 16; o; o >>= 1)
+        x = x + Pair{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
     return x;
 }
 
@@ -82,30 +105,38 @@ struct Row {
 };
 
 // Inclusive sum over the lanes of one warp.
-__device__ __forceinline__ double warp_scan(double x, int lane) {
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const Pair y{__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)};
+        if (lane >= o) x = y + x;
     }
     return x;
 }
 
-// The lane whose share of [0, total) holds t: the first with v > 0 and
-// base + (sum of lanes up to it) > t, else the last with v > 0; -1 if none.
-// Adds the shares before it to base.
-__device__ __forceinline__ int pick(double v, double t, double &base, int lane) {
-    const double incl = base + warp_scan(v, lane);
-    const unsigned some = __ballot_sync(0xffffffffu, v > 0.0);
-    const unsigned past = __ballot_sync(0xffffffffu, v > 0.0 && incl > t);
+// The lane whose share holds t: the first with v > 0 and base + (sum of the lanes up to
+// it) > t, else (past = false) the last with v > 0; -1 if none.  Adds the shares
+// before it to base.  With u >= 0 the threshold is set first: u times the sum of all shares.
+__device__ __forceinline__ int pick(const Pair &v, float u, Pair &t, Pair &base, int lane, bool &past) {
+    const Pair incl = base + warp_scan(v, lane);
+    if (u >= 0.f) t = times(u, shfl(incl, 31));
+    const unsigned some = __ballot_sync(0xffffffffu, v.positive());
+    const unsigned beyond = __ballot_sync(0xffffffffu, v.positive() && incl > t);
+    past = beyond != 0u;
     if (!some) return -1;
-    const int l = past ? __ffs(past) - 1 : 31 - __clz(some);
-    base = __shfl_sync(0xffffffffu, incl - v, l);
+    const int l = beyond ? __ffs(beyond) - 1 : 31 - __clz(some);
+    const Pair before = shfl(incl, max(l - 1, 0));
+    if (l > 0) base = before;
     return l;
 }
 
+// Lane's entry of n sums in shared memory.
+__device__ __forceinline__ Pair from(const float2 *x, int lane, int n) {
+    return lane < n ? Pair{x[lane].x, x[lane].y} : Pair{};
+}
+
 // Sum of entries [i0, i1) of the row over one warp, on every lane.
-__device__ __forceinline__ double run_sum(const Row &row, int i0, int i1, int lane) {
+__device__ __forceinline__ Pair run_sum(const Row &row, int i0, int i1, int lane) {
     Pair acc;
     for (; i0 < i1; i0 += 32 * kLoads) {
         float pv[kLoads], qv[kLoads];
@@ -122,12 +153,12 @@ __device__ __forceinline__ double run_sum(const Row &row, int i0, int i1, int la
             acc.add(d, e);
         }
     }
-    return warp_sum(acc).value();
+    return warp_sum(Pair{} + acc);
 }
 
 __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const AcceptParams P) {
     __shared__ int s_a, s_n, s_x, s_owner;
-    __shared__ double s_warp[kAcceptWarps], s_sub[kAcceptWarps], s_total[2], s_base, s_t;
+    __shared__ float2 s_warp[kAcceptWarps], s_sub[kAcceptWarps], s_total[2], s_base, s_t;
     pdl_wait();
     pdl_launch_dependents();
     cg::cluster_group cluster = cg::this_cluster();
@@ -135,7 +166,9 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const Ac
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t V = P.vocab;
 
+    float u_sample = 0.f;
     if (warp == 0) {
+        u_sample = __saturatef(P.u_sample[b]);
         int n = P.n_draft ? P.n_draft[b] : P.k;
         if (n < 0 || n > P.k) {
             if (lane == 0 && rank == 0) kvq_report(P.err, WM_DEVERR_BAD_LENGTH);
@@ -153,7 +186,8 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const Ac
                 if (ok) {
                     const float pv = __saturatef(P.target_probs[((int64_t)b * (P.k + 1) + j) * V + x]);
                     const float qv = P.draft_probs ? __saturatef(P.draft_probs[((int64_t)b * P.k + j) * V + x]) : 1.f;
-                    ok = (double)u * (double)qv < (double)pv;
+                    const float h = u * qv;
+                    ok = h < pv || (h == pv && fmaf(u, qv, -h) < 0.f);  // u q < p exactly
                 }
             }
             const unsigned bad = __ballot_sync(0xffffffffu, !ok);
@@ -185,33 +219,37 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const Ac
     const int w0 = min(c1, c0 + warp * per_warp), w1 = min(c1, w0 + per_warp);
 
     for (int pass = 0;; ++pass) {
-        const double v = run_sum(row, w0, w1, lane);
-        if (lane == 0) s_warp[warp] = v;
+        const Pair v = run_sum(row, w0, w1, lane);
+        if (lane == 0) s_warp[warp] = make_float2(v.hi, v.lo);
         __syncthreads();
         if (warp == 0) {
-            const double t = __shfl_sync(0xffffffffu, warp_scan(lane < kAcceptWarps ? s_warp[lane] : 0.0, lane), 31);
-            if (lane == 0) s_total[pass] = t;
+            const Pair t = warp_sum(from(s_warp, lane, kAcceptWarps));
+            if (lane == 0) s_total[pass] = make_float2(t.hi, t.lo);
         }
         cluster.sync();
         if (warp == 0) {
-            const double share = lane < n_cta ? *cluster.map_shared_rank(&s_total[pass], lane) : 0.0;
-            const double total = __shfl_sync(0xffffffffu, warp_scan(share, lane), 31);
-            const double t = (double)__saturatef(P.u_sample[b]) * total;
-            double base = 0.0;
-            const int owner = pick(share, t, base, lane);  // -1: no weight at all
+            Pair share;
+            if (lane < n_cta) {
+                const float2 x = *cluster.map_shared_rank(&s_total[pass], lane);
+                share = Pair{x.x, x.y};
+            }
+            Pair t, base;
+            bool past;
+            const int owner = pick(share, u_sample, t, base, lane, past);  // -1: no weight at all
             if (lane == 0) {
                 s_owner = owner;
-                s_base = base;
-                s_t = t;
+                s_base = make_float2(base.hi, base.lo);
+                s_t = make_float2(t.hi, t.lo);
             }
         }
         __syncthreads();
-        cluster.barrier_arrive();  // this CTA has read the others' totals
+        // this CTA has read the others' totals (nothing else is handed over: no release)
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
         if (s_owner >= 0 || (!row.q && row.skip < 0)) break;
         // nothing left where the target exceeds the draft: the target's own row
         row.q = nullptr;
         row.skip = -1;
-        cluster.barrier_wait();
+        asm volatile("barrier.cluster.wait;" ::: "memory");
     }
     const int owner = s_owner;
     int32_t *tokens = P.tokens + (int64_t)b * (P.k + 1);
@@ -228,43 +266,53 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const Ac
         }
     }
     if (owner == rank) {
-        const double t = s_t;
-        double base = s_base;
-        // the warp's run that holds t, its sixteenth, then the entry
-        const int w = pick(lane < kAcceptWarps ? s_warp[lane] : 0.0, t, base, lane);
+        Pair t{s_t.x, s_t.y}, base{s_base.x, s_base.y};
+        // the warp's run that holds t, its part, the lane's eight entries, the entry
+        bool past;
+        const int w = pick(from(s_warp, lane, kAcceptWarps), -1.f, t, base, lane, past);
         const int x0 = c0 + w * per_warp, x1 = min(c1, x0 + per_warp);
         const int per_sub = ((x1 - x0 + kAcceptWarps - 1) / kAcceptWarps + 31) / 32 * 32;
         const int y0 = min(x1, x0 + warp * per_sub);
-        const double v = run_sum(row, y0, min(x1, y0 + per_sub), lane);
-        if (lane == 0) s_sub[warp] = v;
+        const Pair v = run_sum(row, y0, min(x1, y0 + per_sub), lane);
+        if (lane == 0) s_sub[warp] = make_float2(v.hi, v.lo);
         __syncthreads();
         if (warp == 0) {
-            const int s = pick(lane < kAcceptWarps ? s_sub[lane] : 0.0, t, base, lane);
+            const int s = pick(from(s_sub, lane, kAcceptWarps), -1.f, t, base, lane, past);
             const int z0 = x0 + s * per_sub, z1 = min(x1, z0 + per_sub);
             int token = -1;
-            for (int i0 = z0; i0 < z1; i0 += 32) {
-                const int i = i0 + lane;
-                double r = 0.0;
-                if (i < z1) {
-                    float pv, qv, d, e;
-                    row.load(i, pv, qv);
-                    row.weight(pv, qv, i, d, e);
-                    r = (double)d + (double)e;
+            for (int z = z0; z < z1; z += 256) {
+                float pv[8], qv[8];
+                Pair e[8], part;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = z + 8 * lane + j;
+                    pv[j] = qv[j] = 0.f;
+                    if (i < z1) row.load(i, pv[j], qv[j]);
                 }
-                const double incl = base + warp_scan(r, lane);
-                const unsigned some = __ballot_sync(0xffffffffu, r > 0.0);
-                const unsigned past = __ballot_sync(0xffffffffu, r > 0.0 && incl > t);
-                if (past) {
-                    token = i0 + __ffs(past) - 1;
-                    break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    row.weight(pv[j], qv[j], z + 8 * lane + j, e[j].hi, e[j].lo);
+                    part.add(e[j].hi, e[j].lo);
                 }
-                if (some) token = i0 + 31 - __clz(some);  // kept if rounding leaves none past t
-                base = __shfl_sync(0xffffffffu, incl, 31);
+                part = Pair{} + part;
+                const Pair end = base + warp_sum(part);
+                const int l = pick(part, -1.f, t, base, lane, past);
+                if (l < 0) continue;
+                Pair r;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const Pair x = shfl(e[j], l);
+                    if (lane == j) r = x;
+                }
+                const bool found = past;
+                token = z + 8 * l + pick(r, -1.f, t, base, lane, past);
+                if (found) break;
+                base = end;  // the last entry with weight is kept if rounding leaves none past t
             }
             if (lane == 0) tokens[a] = token;
         }
     }
-    cluster.barrier_wait();  // no CTA leaves while another may still read its total
+    asm volatile("barrier.cluster.wait;" ::: "memory");  // no CTA leaves while another may still read its total
 }
 
 }  // namespace
