@@ -416,11 +416,11 @@ size_t wm_kvq_record_bytes(int32_t head_dim);
  * lengths first; layers that share them append one after the other).  Tokens
  * whose position would be negative are padding and are skipped.
  *   k_new, v_new  [batch][n_new][n_kv_heads][head_dim] bf16, 16-byte aligned.
- * Per token, head and K or V, over the channels x_d, with the arithmetic of
- * real numbers (the result is the same bits on every call):
- *   z = min x_d;  s = bf16((max x_d - z) / 15), to nearest even;
- *   c_d = min(15, max(0, rint((x_d - z) / s))), ties to even;  c_d = 0 if s = 0.
- * (Differences and quotients as doubles give them.)  A row that holds a NaN or an infinity
+ * Per token, head and K or V, over the channels x_d (the same bits on every call):
+ *   z = min x_d;  s = (max x_d - z) / 15 rounded to bf16 (nearest even);
+ *   c_d = min(15, max(0, rint(t_d / s))), t_d = x_d - z in fp32, the quotient
+ *   exact and ties to even;  c_d = 0 if s = 0.
+ * The range and its fifteenth are as doubles give them.  A row that holds a NaN or an infinity
  * gets s = z = NaN and attention over it gives NaN.  Other positions of the
  * records keep their codes.  A seq_lens[b] that is negative or beyond the capacity records
  * WM_DEVERR_BAD_LENGTH and nothing is written for b; a block-table entry

@@ -8,15 +8,21 @@
 // the range still fits (c is clamped).  A row with a NaN or an infinity gets
 // s = z = NaN: whoever attends to it sees NaN, as with a bf16 cache.
 //
-// Codes and scales are those of the definition in 64 bits, bit for bit: both
-// are computed in fp32, and where that lands next to a rounding border (where
-// its error could choose the other side) it is decided exactly -- an element by the
-// sign of (x - z) - h s at the half h, which one FMA gives exactly when x - z is
-// exact, else and for the scale in doubles.  (Exact ties are common in bf16 data, a few
-// per thousand elements, and this GPU has 2 FP64 units per SM.)
+// Codes and scales are those of the definition, bit for bit.  With t = x - z
+// (rounded to fp32; exact unless x is below 2^-16 of z) the quotient t / s is taken
+// in fp32 with one Newton step, so an exact tie -- common in bf16 data, one or two per
+// hundred elements -- comes out as k + 1/2 exactly and rounds to even.  The code r is then
+// right if |t - r s| <= s / 2, which one FMA gives exactly; else it is one off.  The
+// scale is taken again in doubles where fp32 lands next to the middle of two bf16
+// values.  (This GPU has 2 FP64 units per SM: doubles for every tie took
+// three quarters of the time.)
 //
-// One CTA handles one record (64 positions of one KV head), a warp the K and the V row
-// of a token at a time.  K's words go to a shared image of the record's K area,
+// One CTA handles one record (64 positions of one KV head).  A lane holds 8 channels (one
+// 16-byte load), D / 8 lanes a row, so a warp quantises the K and V rows of 256 / D
+// tokens at a time: the work per row (range, scale, reciprocal) is the longer half, and
+// rows side by side share its instructions.  Least and largest run as one packed bf16 pair
+// (min, -max).  A prompt of 32K tokens with 8 heads of 128 took 94 us with a row per
+// warp and fp32 ranges, 144 instructions a row.  K's words go to a shared image of the record's K area,
 // V's codes to a byte matrix from which a thread takes 4 channels x 8 positions and
 // transposes them into 4 words (the cache holds V transposed).  A V word of which the append
 // covers only some positions is read, merged and written back, so the other
@@ -35,29 +41,34 @@ namespace wm {
 
 namespace {
 
-// Twice the fp32 error of (x - z) / s <= 15.1 (difference, reciprocal, product: 2^-22 of it).
-constexpr float kBorder = 1.f / 131072.f;
-
-// Least and largest of one value per lane; NaN if any is.
-__device__ __forceinline__ float warp_min(float x) {
-    float y;
-    asm volatile("redux.sync.min.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ float rcp(float x) {
     float y;
@@ -80,79 +91,62 @@ __device__ __forceinline__ float row_scale(float lo, float hi) {
     return __bfloat162float(__float2bfloat16_rn(s));
 }
 
-// The code of an element next to a border (or, with !simple, of any).
-__device__ __noinline__ uint32_t code_exactly(float x, float z, float s, float y, bool simple) {
-    const float t = x - z;
-    if (simple) {
-        const float bb = t - x;
-        const float lost = (x - (t - bb)) - (z + bb);  // of the difference's rounding
-        if (lost == 0.f) {
-            const float below = floorf(y), d = fmaf(-(below + 0.5f), s, t);
-            const int c = (int)below;
-            return (uint32_t)min(15, max(0, d > 0.f ? c + 1 : d < 0.f ? c : c + (c & 1)));
-        }
-    }
-    return (uint32_t)fmin(fmax(rint(((double)x - (double)z) / (double)s), 0.0), 15.0);
-}
+// 1.5 x 2^23: added to a y below 2^22 it leaves y, rounded to even, in the low bits.
+constexpr float kMagic = 12582912.f;
+constexpr uint32_t kMagicBits = 0x4b400000u;
 
-// Codes of one warp's row, NE consecutive channels per lane; also its scale and zero.
-template <int NE>
-__device__ __forceinline__ void quantise_row(const float (&x)[NE], uint32_t (&c)[NE], float &s, float &z) {
-    float lo = x[0], hi = x[0];
+// Codes of a row of D channels, 8 per lane as bf16 pairs, on D / 8 neighbouring lanes;
+// each code i as m[i] = kMagicBits + code.  Also the row's scale and zero.
+template <int D>
+__device__ __forceinline__ void quantise_row(const uint4 &in, uint32_t (&m)[8], float &s, float &z) {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    // least of the values and of their negatives (exact), a pair of channels at a time
+    uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
+    uint32_t hi = min2_nan(min2_nan(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
+                           min2_nan(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
+    uint32_t range = min2_nan(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));  // (min, -max)
 #pragma unroll
-    for (int i = 1; i < NE; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
-    z = warp_min(lo);
-    hi = warp_max(hi);
+    for (int o = D / 16; o; o >>= 1) range = min2_nan(range, __shfl_xor_sync(0xffffffffu, range, o));
+    z = __uint_as_float(range << 16);
+    const float top = -__uint_as_float(range & 0xffff0000u);
 #pragma unroll
-    for (int i = 0; i < NE; ++i) c[i] = 0u;
-    if (!(hi - hi == 0.f && z - z == 0.f)) {  // a NaN or an infinity
+    for (int i = 0; i < 8; ++i) m[i] = kMagicBits;
+    if (!(top - top == 0.f && z - z == 0.f)) {  // a NaN or an infinity
         s = z = CUDART_NAN_F;
         return;
     }
-    s = row_scale(z, hi);
+    s = row_scale(z, top);
     if (!(s > 0.f)) return;
     const float rs = rcp(s);
-    const bool simple = s > 1e-30f && s < 1e30f;  // else: quotients in doubles
-    bool near = !simple;
-    float y[NE];
+    const bool simple = s > 1e-28f && s < 1e30f;  // else: quotients in doubles
+    const uint64_t nz2 = pack2(-z, -z), rs2 = pack2(rs, rs), ns2 = pack2(-s, -s);
+    const uint64_t magic2 = pack2(kMagic, kMagic), unmagic2 = pack2(-kMagic, -kMagic);
+    const float half = 0.5f * s;
+    bool off = !simple;  // a code that may be one off
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-        constexpr float kMagic = 12582912.f;  // 1.5 x 2^23: the sum's low bits are y rounded to even
-        y[i] = (x[i] - z) * rs;
-        const float m = y[i] + kMagic;
-        c[i] = __float_as_uint(m) & 15u;
-        near |= fabsf(y[i] - (m - kMagic)) > 0.5f - kBorder;
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t t2 = add2(pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), nz2);
+        uint64_t y2 = mul2(t2, rs2);
+        y2 = fma2(fma2(y2, ns2, t2), rs2, y2);
+        const uint64_t m2 = add2(y2, magic2);
+        float a, b, d, e;
+        unpack2(m2, a, b);
+        m[2 * i] = __float_as_uint(a);
+        m[2 * i + 1] = __float_as_uint(b);
+        unpack2(fma2(add2(m2, unmagic2), ns2, t2), d, e);
+        off |= fabsf(d) > half || fabsf(e) > half;
     }
-    if (near) {
+    if (off) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i)
-            if (!simple || fabsf(y[i] - rintf(y[i])) > 0.5f - kBorder) c[i] = code_exactly(x[i], z, s, y[i], simple);
-    }
-}
-
-template <int NE>
-__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, int lane, float (&x)[NE]) {
-    uint32_t w[NE / 2];
-    if constexpr (NE == 2) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p) + lane);
-    } else if constexpr (NE == 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + lane);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + lane);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    }
-#pragma unroll
-    for (int i = 0; i < NE / 2; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 8; ++i) {
+            const float t = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) - z;
+            if (simple) {
+                const float d = fmaf((float)(int)(m[i] - kMagicBits), -s, t);
+                m[i] += d > half ? 1u : d < -half ? ~0u : 0u;
+            } else {
+                m[i] = kMagicBits + (uint32_t)fmin(fmax(rint((double)t / (double)s), 0.0), 15.0);
+            }
+        }
     }
 }
 
@@ -163,6 +157,21 @@ __device__ __forceinline__ uint32_t pack_sz(float s, float z) {
 
 // Bit position of element e in its word.
 __host__ __device__ constexpr int nib_bit(int e) { return 4 * ((e & 7) / 2 + 4 * (e & 1)); }
+
+// Sum of m[i] 2^bit(i) less the kMagicBits in it, modulo 2^32: the codes at their bits.
+__device__ __forceinline__ uint32_t pack_nibbles(const uint32_t (&m)[8]) {
+    uint32_t sub = 0u, w = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sub += kMagicBits << nib_bit(i);
+    w -= sub;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w += m[i] << nib_bit(i);
+    return w;
+}
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    constexpr uint32_t sub = kMagicBits + (kMagicBits << 8) + (kMagicBits << 16) + (kMagicBits << 24);
+    return a + (b << 8) + (c << 16) + (d << 24) - sub;
+}
 
 // 4 channels (bytes) of 8 positions a[0..7] into 4 words of 8 codes.
 __device__ __forceinline__ void transpose_codes(const uint32_t (&a)[8], uint32_t (&w)[4]) {
@@ -179,7 +188,7 @@ __device__ __forceinline__ void transpose_codes(const uint32_t (&a)[8], uint32_t
 template <int D>
 __global__ void kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restrict__ kn,
                                   const __nv_bfloat16 *__restrict__ vn, int n_new, int32_t *__restrict__ err) {
-    constexpr int NE = D / 32;
+    constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes per row, rows per warp
     constexpr int VS = D + 4;  // bytes per row of V codes: 8 rows down is 8 banks on
     __shared__ __align__(16) uint32_t s_k[8 * D];               // K area image: [D / 32][64][4 words]
     __shared__ __align__(16) uint8_t s_v[kRecKeys * VS];        // V codes: [64][D]
@@ -205,40 +214,30 @@ __global__ void kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restri
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
     const int64_t row0 = ((int64_t)b * n_new + blk * kRecKeys - pos0) * c.n_kv_heads + h;  // input row of record row 0
-    for (int r = r0 + warp; r < r1; r += n_warps) {
-        const int64_t at = (row0 + (int64_t)r * c.n_kv_heads) * D;
-        float xk[NE], xv[NE];
-        load_row<NE>(kn + at, lane, xk);
-        load_row<NE>(vn + at, lane, xv);
-        uint32_t ck[NE], cv[NE];
+    const int word = lane % LANES;  // of the row's D / 8
+    for (int rb = r0 + warp * ROWS; rb < r1; rb += n_warps * ROWS) {
+        const int r = rb + lane / LANES;
+        const bool valid = r < r1;
+        uint4 xk = make_uint4(0u, 0u, 0u, 0u), xv = xk;
+        if (valid) {
+            const int64_t at = (row0 + (int64_t)r * c.n_kv_heads) * D;
+            xk = __ldg(reinterpret_cast<const uint4 *>(kn + at) + word);
+            xv = __ldg(reinterpret_cast<const uint4 *>(vn + at) + word);
+        }
+        uint32_t mk[8], mv[8];
         float sk, zk, sv, zv;
-        quantise_row<NE>(xk, ck, sk, zk);
-        quantise_row<NE>(xv, cv, sv, zv);
-        if (lane == 0) {
-            s_sz[0][r] = pack_sz(sk, zk);
-            s_sz[1][r] = pack_sz(sv, zv);
+        quantise_row<D>(xk, mk, sk, zk);
+        quantise_row<D>(xv, mv, sv, zv);
+        if (valid) {
+            s_k[(word >> 2) * 256 + r * 4 + (word & 3)] = pack_nibbles(mk);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(s_v + r * VS + word * 8);
+            dst[0] = pack_bytes(mv[0], mv[1], mv[2], mv[3]);
+            dst[1] = pack_bytes(mv[4], mv[5], mv[6], mv[7]);
+            if (word == 0) {
+                s_sz[0][r] = pack_sz(sk, zk);
+                s_sz[1][r] = pack_sz(sv, zv);
+            }
         }
-        uint8_t *dst = s_v + r * VS + lane * NE;
-        if constexpr (NE == 2) {
-            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)(cv[0] | (cv[1] << 8));
-        } else {
-#pragma unroll
-            for (int i = 0; i < NE; i += 4)
-                *reinterpret_cast<uint32_t *>(dst + i) =
-                    cv[i] | (cv[i + 1] << 8) | (cv[i + 2] << 16) | (cv[i + 3] << 24);
-        }
-        // this lane's part of a K word, joined with the neighbours that share it
-        uint32_t w = 0u;
-#pragma unroll
-        for (int i = 0; i < NE; ++i) w |= ck[i] << nib_bit(i);
-        if constexpr (NE == 2) {
-            w <<= 4 * (lane & 3);
-            w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        }
-        if constexpr (NE == 4) w <<= 8 * (lane & 1);
-        if constexpr (NE <= 4) w |= __shfl_xor_sync(0xffffffffu, w, 1);
-        const int word = lane * NE / 8;  // of the row's D / 8
-        if (lane * NE % 8 == 0) s_k[(word >> 2) * 256 + r * 4 + (word & 3)] = w;
     }
     __syncthreads();
     // K units of the covered positions

@@ -42,7 +42,8 @@ def quantise(x: torch.Tensor):
     s_bits = to_bf16_bits((y.max(-1) - z) / 15.0)
     s = from_bits(s_bits)
     with np.errstate(divide="ignore", invalid="ignore"):
-        c = np.where(s[..., None] > 0, np.rint((y - z[..., None]) / s[..., None]), 0.0)
+        t = (y - z[..., None]).astype(np.float32).astype(np.float64)  # the difference is fp32's
+        c = np.where(s[..., None] > 0, np.rint(t / s[..., None]), 0.0)
     c = np.clip(c, 0, 15).astype(np.uint8)
     z_bits = (z.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
     return c, np.where(bad, 0x7FFF, s_bits).astype(np.uint16), np.where(bad, 0x7FFF, z_bits).astype(np.uint16)
