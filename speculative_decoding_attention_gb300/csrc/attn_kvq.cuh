@@ -27,6 +27,13 @@
 // a product with a constant operand, free on the tensor cores.  A row of constant
 // values has s_V = 0 and codes 0; a stand-in scale |z| / 256 carries its zero.
 //
+// The tensor cores add to O by cutting off, not rounding, so a long chain of additions
+// drifts: averages over a million random values were off by 0.7% after 432 tiles, where bf16
+// rounds by 0.17%.  Every
+// kKvqChain tiles the softmax warps therefore add O to fp32 sums of their own (rounded, in
+// the part's slot of the workspace, which each thread alone touches) and the products start
+// O anew.  (LONG: the kernel for capacities at which a part can be longer than that.)
+//
 // Each CTA takes one run of the batch's tiles (kvq_schedule), cut into parts at
 // (sequence, KV head) borders; every role counts tiles across parts, so no
 // buffer drains at a border.  Roles:
@@ -92,7 +99,7 @@ struct KvqCfg {
     // behind the stages: per-key constants, per-row scratch, barriers
     static constexpr int CONST_BYTES = 4 * 128 * 20;
     static constexpr int RED_BYTES = 8 * NR * 4, ROW_BYTES = 2 * NR * 4;
-    static constexpr int TAIL = CONST_BYTES + RED_BYTES + 2 * ROW_BYTES + 256 + 512 + 32 * 8 + 64;
+    static constexpr int TAIL = CONST_BYTES + RED_BYTES + 3 * ROW_BYTES + 256 + 512 + 32 * 8 + 64;
     static constexpr int ROOM = 227 * 1024 - 1024 - PT_OFF - TAIL;
     // A second P' buffer if four stages still fit (the softmax of a tile then need not
     // wait for the products of the last), then up to eight stages.
@@ -105,7 +112,8 @@ struct KvqCfg {
     static constexpr int RED_OFF = CONST_OFF + CONST_BYTES;       // float [2][NR][4]: per row and lane quadrant
     static constexpr int ZQ_OFF = RED_OFF + RED_BYTES;            // float [2][NR]: sums of a part's queries
     static constexpr int NM_OFF = ZQ_OFF + ROW_BYTES;             // float [2][NR]: minus (running maximum - kKvqOff)
-    static constexpr int FLAG_OFF = NM_OFF + ROW_BYTES;           // int [64]: [0] abort, [8 + w] scratch
+    static constexpr int NP_OFF = NM_OFF + ROW_BYTES;             // float [2][NR]: the same when O was last taken over
+    static constexpr int FLAG_OFF = NP_OFF + ROW_BYTES;           // int [64]: [0] abort, [8 + w] scratch
     static constexpr int BAR_OFF = FLAG_OFF + 256;
     static constexpr int NBAR = 2 * NST + 8 + 8 + 1 + 1 + 2 + 2 + 1 + 2;
     static_assert(NBAR * 8 <= 512, "barriers");
@@ -242,7 +250,7 @@ __device__ __forceinline__ bool kvq_wait_slow(uint32_t bar, uint32_t parity, uin
     return false;
 }
 
-template <int D, int NR>
+template <int D, int NR, bool LONG>
 __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(const KvqAttnParams p) {
     using C = KvqCfg<D, NR>;
     constexpr int TK = kKvqTile, NC = C::NC, HR = C::HR, NSW = C::NSW, ND = C::ND, NST = C::NST, NPB = C::NPB;
@@ -255,6 +263,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     const uint32_t s_red = sbase + C::RED_OFF;              // float [2][NR][4]
     const uint32_t s_zq = sbase + C::ZQ_OFF;                // float [2][NR]
     const uint32_t s_nm = sbase + C::NM_OFF;                // float [2][NR]
+    const uint32_t s_np = sbase + C::NP_OFF;                // float [2][NR]
     const uint32_t s_const = sbase + C::CONST_OFF;          // float4 [4][128]
     const uint32_t s_zr = s_const + 4 * 128 * 16;           // float [4][128]
     volatile int *flags = reinterpret_cast<volatile int *>(gb + C::FLAG_OFF);
@@ -457,7 +466,8 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {  // 16 keys each
                                 const uint64_t bp = pb + ((kk * 2 * C::PT_ATOM) >> 4);
-                                mma_f16_ts(d, a + 8 * kk, bp, id_pv, t > 0 || j > 0 || kk > 0);
+                                mma_f16_ts(d, a + 8 * kk, bp, id_pv,
+                                           (LONG ? t % kKvqChain : t) > 0 || j > 0 || kk > 0);
                                 mma_f16_ts(d, tmem + C::E_COL, bp, id_pv, 1u);
                             }
                             tc::commit(bar_afree + 8 * (C::KS + slot));
@@ -661,9 +671,52 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             uint64_t l2[HR / 2], z2[HR / 2];  // sums of P' / s_V and P' z_V / s_V, two rows each
 #pragma unroll
             for (int i = 0; i < HR / 2; ++i) l2[i] = z2[i] = 0;
+            const int64_t seg = (int64_t)blockIdx.x + (int64_t)q.b * p.c.n_kv_heads + q.h;
+            // What was taken over of O before (n_over times, at least once), for 8 rows at the present
+            // maxima, added to o8.
+            const auto add_over = [&](int c, int j, int n_over, float (&o8)[8]) {
+                const int d = c * 128 + kt;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + 8 * j + i;
+                    if (r >= p.rows || (D == 64 && d >= 64)) continue;
+                    const float np = ld_shared_f32(s_np + (((n_over - 1) & 1) * NR + r) * 4);
+                    o8[i] = fmaf(p.o_part[(seg * p.rows + r) * D + d], ex2(ld_shared_f32(nm + 4 * (8 * j + i)) - np),
+                                 o8[i]);
+                }
+            };
             for (int t = 0; t < n; ++t) {
                 const int gt = g + t;
                 const int key0 = key_first + t * TK;
+
+                if (LONG && __builtin_expect(t > 0 && t % kKvqChain == 0, 0)) {
+                    // take O over (it is at the maxima of the last tile, which are still the present ones)
+                    wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
+                    __syncwarp();
+                    tc::fence_after_sync();
+                    const int n_over = t / kKvqChain - 1;
+#pragma unroll 1
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll 1
+                        for (int j = 0; j < HR / 8; ++j) {
+                            float o8[8];
+                            tc::ld_32x32b_x8(tmem + lane_off + C::O_COL + c * NR + r0 + 8 * j, o8);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o8[i] *= 16777216.f;
+                            if (n_over > 0) add_over(c, j, n_over, o8);
+                            const int d = c * 128 + kt;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int r = r0 + 8 * j + i;
+                                if (r < p.rows && (D > 64 || d < 64)) p.o_part[(seg * p.rows + r) * D + d] = o8[i];
+                            }
+                        }
+                    // (read by the next one, many barriers from here)
+                    if (q4 == 0 && lane < HR)
+                        st_shared_f32(s_np + ((n_over & 1) * NR + r0 + lane) * 4, ld_shared_f32(nm + 4 * lane));
+                    tc::fence_before_sync();
+                }
 
                 wait(bar_sfull, gt);
                 __syncwarp();
@@ -741,16 +794,18 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     }
                     if (q4 == 0 && lane < HR) st_shared_f32(nm + 4 * lane, ld_shared_f32(nm + 4 * lane) - up(lane));
                     if (t > 0) {
-                        // O holds this part's tiles so far at the old maxima
-                        wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
-                        __syncwarp();
-                        tc::fence_after_sync();
 #pragma unroll
                         for (int i = 0; i < HR / 2; ++i) {
                             const uint64_t al = pack2(ex2(-up(2 * i)), ex2(-up(2 * i + 1)));
                             l2[i] = mul2(l2[i], al);
                             z2[i] = mul2(z2[i], al);
                         }
+                    }
+                    if ((LONG ? t % kKvqChain : t) > 0) {
+                        // O holds tiles at the old maxima
+                        wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
+                        __syncwarp();
+                        tc::fence_after_sync();
 #pragma unroll
                         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -800,7 +855,6 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 if (lane == 0) mbar_arrive(bar_pfull + 8 * (gt % NPB));
             }
 
-            const int64_t seg = (int64_t)blockIdx.x + (int64_t)q.b * p.c.n_kv_heads + q.h;
             have = walk.next(p.c, q);
             // The next part's queries, while the last P.V runs: the last S of this part
             // was read above, so every S that used the query buffer is complete.
@@ -847,13 +901,15 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     float o8[8];
                     tc::ld_32x32b_x8(tmem + lane_off + C::O_COL + c * NR + r0 + 8 * j, o8);
                     tc::wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o8[i] = fmaf(o8[i], 16777216.f, z8[i]);
+                    if (LONG && __builtin_expect(n > kKvqChain, 0)) add_over(c, j, (n - 1) / kKvqChain, o8);
                     const int d = c * 128 + kt;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = r0 + 8 * j + i;
                         if (r >= p.rows || (D == 64 && d >= 64)) continue;
-                        p.o_part[(seg * p.rows + r) * D + d] =
-                            l8[i] == 0.f ? 0.f : fmaf(o8[i], 16777216.f, z8[i]) / l8[i];
+                        p.o_part[(seg * p.rows + r) * D + d] = l8[i] == 0.f ? 0.f : o8[i] / l8[i];
                     }
                 }
 #pragma unroll
@@ -878,7 +934,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     }
 }
 
-template <int D, int NR>
+template <int D, int NR, bool LONG>
 cudaError_t launch_kvq_attn_nr(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
     constexpr int smem = KvqCfg<D, NR>::TOTAL;
     static bool configured[64] = {};
@@ -887,20 +943,20 @@ cudaError_t launch_kvq_attn_nr(const KvqAttnParams &p, int n_cta, cudaStream_t s
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    return launch_pdl(kvq_attn_kernel<D, NR>, dim3(n_cta), dim3(KvqCfg<D, NR>::THREADS), smem, stream, p);
+    return launch_pdl(kvq_attn_kernel<D, NR, LONG>, dim3(n_cta), dim3(KvqCfg<D, NR>::THREADS), smem, stream, p);
 }
 
-template <int D>
+template <int D, bool LONG>
 cudaError_t launch_kvq_attn_d(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
     switch ((p.rows + 15) / 16) {
-        case 1: return launch_kvq_attn_nr<D, 16>(p, n_cta, stream);
-        case 2: return launch_kvq_attn_nr<D, 32>(p, n_cta, stream);
-        case 3: return launch_kvq_attn_nr<D, 48>(p, n_cta, stream);
-        case 4: return launch_kvq_attn_nr<D, 64>(p, n_cta, stream);
+        case 1: return launch_kvq_attn_nr<D, 16, LONG>(p, n_cta, stream);
+        case 2: return launch_kvq_attn_nr<D, 32, LONG>(p, n_cta, stream);
+        case 3: return launch_kvq_attn_nr<D, 48, LONG>(p, n_cta, stream);
+        case 4: return launch_kvq_attn_nr<D, 64, LONG>(p, n_cta, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -1,0 +1,10 @@
+// attn_kvq_long_d256.cu -- attention over the 4-bit cache, head_dim 256, parts of any length.
+#include "attn_kvq.cuh"
+
+namespace wm {
+
+cudaError_t launch_kvq_attn_long_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
+    return launch_kvq_attn_d<256, true>(p, n_cta, stream);
+}
+
+}  // namespace wm
