@@ -524,9 +524,9 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     const float ks = __uint_as_float(ksz << 16), kz = __uint_as_float(ksz & 0xffff0000u);
                     const float vs = __uint_as_float(vsz << 16), vz = __uint_as_float(vsz & 0xffff0000u);
                     // Scale 0 (constant values, codes 0): a stand-in that keeps z / s in
-                    // range.  At least 2^-90, which keeps the sums of P' / s below fp32's
-                    // largest: values are off by 15 x 2^-90 where a scale is smaller.
-                    const float se = fmaxf(vs > 0.f ? vs : fabsf(vz) * 0.00390625f, 8.0779357e-28f);
+                    // range.  At least 2^-86, which keeps the sums of P' / s below fp32's
+                    // largest: values are off by 15 x 2^-86 where a scale is smaller.
+                    const float se = fmaxf(vs > 0.f ? vs : fabsf(vz) * 0.00390625f, 1.2924697e-26f);
                     const bool by16 = L & 2;  // this key's V codes are 16 times too large: P' is divided by 16
                     const float up = by16 ? 16.f : 1.f;
                     float inv = rcp(se) * up, zr = fmaf(vz, inv, 8.f * up);

@@ -18,18 +18,21 @@
 // three quarters of the time.)
 //
 // One CTA handles one record (64 positions of one KV head).  A lane holds 8 channels (one
-// 16-byte load), D / 8 lanes a row, so a warp quantises the K and V rows of 256 / D
-// tokens at a time: the work per row (range, scale, reciprocal) is the longer half, and
-// rows side by side share its instructions.  Least and largest run as one packed bf16 pair
-// (min, -max).  A prompt of 32K tokens with 8 heads of 128 took 94 us with a row per
-// warp and fp32 ranges, 144 instructions a row.  K's words go to a shared image of the record's K area,
-// V's codes to a byte matrix from which a thread takes 4 channels x 8 positions and
+// 16-byte load), D / 8 lanes a row, so a warp takes the K and V rows of 256 / D tokens at a
+// time and rows side by side share the instructions per row (range, scale, reciprocal);
+// even lanes do them for K, odd ones for V, and exchange the results.  Least and greatest
+// run as one packed bf16 pair (min, -max).  K's words go to a shared image of the record's
+// K area, V's codes to a byte matrix from which a thread takes 4 channels x 8 positions and
 // transposes them into 4 words (the cache holds V transposed).  A V word of which the append
 // covers only some positions is read, merged and written back, so the other
 // positions of the record keep their codes.  One CTA owns a record, so no two
 // write one word.
-// What bounds it: HBM for a prompt (4 D bytes read, D + 8 written per token and head),
-// the launch for a step's few tokens.
+// A prompt of 32K tokens with 8 heads of 128: 51 us, where HBM would take 25 for its 170 MB;
+// instructions bound it (76% of the issue slots; 168 for 16 channels of a lane).  With the
+// row's work done by every lane it was 62, with a row per warp and fp32 ranges 94; with 4
+// CTAs per SM, which need not spill, 4 us more than with 6.  Reading it back as bf16: 26 us,
+// HBM's rate (38 with fp32 arithmetic and stores of 4 bytes, 33 with loads behind the
+// barrier).  For a step's few tokens the launch is the time.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -44,6 +47,11 @@ namespace {
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     uint32_t y;
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
 // Two fp32 operations in one instruction.
@@ -76,53 +84,54 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// bf16 of (hi - lo) / 15, the quotient as in 64 bits.  The fp32 product with 1 / 15 is
-// within 3 of its last places; only one that close to the middle of two bf16
-// values (or too small or large for that) is taken again in doubles, and
-// rounded to bf16 once: through fp32 rounded to odd.
-__device__ __forceinline__ float row_scale(float lo, float hi) {
-    float s = (hi - lo) * (1.f / 15.f);
+__device__ __forceinline__ uint32_t pack_sz(float s, float z) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(s, z);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Least value of this lane's 8 channels of a row and minus the greatest (exact), as a bf16 pair.
+__device__ __forceinline__ uint32_t lane_range(const uint4 &in) {
+    const uint32_t lo = min2_nan(min2_nan(in.x, in.y), min2_nan(in.z, in.w));
+    const uint32_t hi = 0x80008000u ^ max2_nan(max2_nan(in.x, in.y), max2_nan(in.z, in.w));
+    return min2_nan(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+}
+
+// Scale and zero of a row from its range, and 1 / s.  s is bf16 of the range over 15, the
+// quotient as in 64 bits: the fp32 product with 1 / 15 is within 3 of its last places, and
+// only one that close to the middle of two bf16 values (or too small or large for
+// that) is taken again in doubles, and rounded to bf16 once: through fp32 rounded to odd.
+// A scale that the fp32 quotients are not for gets NaN as 1 / s.
+__device__ __forceinline__ void row_scale(uint32_t range, uint32_t &sz, float &rs) {
+    const float z = __uint_as_float(range << 16), top = -__uint_as_float(range & 0xffff0000u);
+    float s = (top - z) * (1.f / 15.f);
     const uint32_t low = __float_as_uint(s) & 0xffffu;
-    if (!(s > 1e-30f && s < 1e37f) || (low >= 0x7ff8u && low <= 0x8008u)) {
-        const double d = ((double)hi - (double)lo) / 15.0;
+    if (!(s > 1e-28f && s < 1e30f) || (low >= 0x7ff8u && low <= 0x8008u)) {
+        if (!(top - top == 0.f && z - z == 0.f)) {  // a NaN or an infinity
+            sz = pack_sz(CUDART_NAN_F, CUDART_NAN_F);
+            rs = CUDART_NAN_F;
+            return;
+        }
+        const double d = ((double)top - (double)z) / 15.0;
         s = __double2float_rz(d);
         if ((double)s != d) s = __uint_as_float(__float_as_uint(s) | 1u);
     }
-    return __bfloat162float(__float2bfloat16_rn(s));
+    sz = pack_sz(s, z);
+    s = __uint_as_float(sz << 16);
+    rs = s > 1e-28f && s < 1e30f ? rcp(s) : CUDART_NAN_F;
 }
 
 // 1.5 x 2^23: added to a y below 2^22 it leaves y, rounded to even, in the low bits.
 constexpr float kMagic = 12582912.f;
 constexpr uint32_t kMagicBits = 0x4b400000u;
 
-// Codes of a row of D channels, 8 per lane as bf16 pairs, on D / 8 neighbouring lanes;
-// each code i as m[i] = kMagicBits + code.  Also the row's scale and zero.
-template <int D>
-__device__ __forceinline__ void quantise_row(const uint4 &in, uint32_t (&m)[8], float &s, float &z) {
+// Codes of 8 channels of a row, each code i as m[i] = kMagicBits + code.
+__device__ __forceinline__ void row_codes(const uint4 &in, uint32_t sz, float rs, uint32_t (&m)[8]) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-    // least of the values and of their negatives (exact), a pair of channels at a time
-    uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
-    uint32_t hi = min2_nan(min2_nan(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
-                           min2_nan(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
-    uint32_t range = min2_nan(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));  // (min, -max)
-#pragma unroll
-    for (int o = D / 16; o; o >>= 1) range = min2_nan(range, __shfl_xor_sync(0xffffffffu, range, o));
-    z = __uint_as_float(range << 16);
-    const float top = -__uint_as_float(range & 0xffff0000u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = kMagicBits;
-    if (!(top - top == 0.f && z - z == 0.f)) {  // a NaN or an infinity
-        s = z = CUDART_NAN_F;
-        return;
-    }
-    s = row_scale(z, top);
-    if (!(s > 0.f)) return;
-    const float rs = rcp(s);
-    const bool simple = s > 1e-28f && s < 1e30f;  // else: quotients in doubles
+    const float s = __uint_as_float(sz << 16), z = __uint_as_float(sz & 0xffff0000u);
     const uint64_t nz2 = pack2(-z, -z), rs2 = pack2(rs, rs), ns2 = pack2(-s, -s);
     const uint64_t magic2 = pack2(kMagic, kMagic), unmagic2 = pack2(-kMagic, -kMagic);
     const float half = 0.5f * s;
-    bool off = !simple;  // a code that may be one off
+    float worst = 0.f;  // largest |t - r s|
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t t2 = add2(pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), nz2);
@@ -134,25 +143,20 @@ __device__ __forceinline__ void quantise_row(const uint4 &in, uint32_t (&m)[8], 
         m[2 * i] = __float_as_uint(a);
         m[2 * i + 1] = __float_as_uint(b);
         unpack2(fma2(add2(m2, unmagic2), ns2, t2), d, e);
-        off |= fabsf(d) > half || fabsf(e) > half;
+        worst = fmaxf(worst, fmaxf(fabsf(d), fabsf(e)));
     }
-    if (off) {
+    if (worst > half || !(rs == rs)) {  // a code that may be one off, or quotients that are not for fp32
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float t = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) - z;
-            if (simple) {
+            if (rs == rs) {
                 const float d = fmaf((float)(int)(m[i] - kMagicBits), -s, t);
                 m[i] += d > half ? 1u : d < -half ? ~0u : 0u;
-            } else {
-                m[i] = kMagicBits + (uint32_t)fmin(fmax(rint((double)t / (double)s), 0.0), 15.0);
+            } else {  // no range (s = 0) or not finite: 0; else the quotient in doubles
+                m[i] = kMagicBits + (s > 0.f ? (uint32_t)fmin(fmax(rint((double)t / (double)s), 0.0), 15.0) : 0u);
             }
         }
     }
-}
-
-__device__ __forceinline__ uint32_t pack_sz(float s, float z) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(s, z);
-    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Bit position of element e in its word.
@@ -185,9 +189,12 @@ __device__ __forceinline__ void transpose_codes(const uint32_t (&a)[8], uint32_t
     w[3] = __byte_perm(h0, h1, 0x7632);
 }
 
+constexpr int kAppendWarps = 8;
+
 template <int D>
-__global__ void kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restrict__ kn,
-                                  const __nv_bfloat16 *__restrict__ vn, int n_new, int32_t *__restrict__ err) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 6)
+    kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restrict__ kn, const __nv_bfloat16 *__restrict__ vn,
+                      int n_new, int32_t *__restrict__ err) {
     constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes per row, rows per warp
     constexpr int VS = D + 4;  // bytes per row of V codes: 8 rows down is 8 banks on
     __shared__ __align__(16) uint32_t s_k[8 * D];               // K area image: [D / 32][64][4 words]
@@ -224,27 +231,33 @@ __global__ void kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restri
             xk = __ldg(reinterpret_cast<const uint4 *>(kn + at) + word);
             xv = __ldg(reinterpret_cast<const uint4 *>(vn + at) + word);
         }
+        // Even lanes reduce K's range and find its scale, odd lanes V's.
+        const uint32_t rk = lane_range(xk), rv = lane_range(xv);
+        const bool odd = lane & 1;
+        uint32_t range = min2_nan(odd ? rv : rk, __shfl_xor_sync(0xffffffffu, odd ? rk : rv, 1));
+#pragma unroll
+        for (int o = LANES / 2; o > 1; o >>= 1) range = min2_nan(range, __shfl_xor_sync(0xffffffffu, range, o));
+        uint32_t sz;
+        float rs;
+        row_scale(range, sz, rs);
+        const uint32_t sz2 = __shfl_xor_sync(0xffffffffu, sz, 1);
+        const float rs2 = __shfl_xor_sync(0xffffffffu, rs, 1);
         uint32_t mk[8], mv[8];
-        float sk, zk, sv, zv;
-        quantise_row<D>(xk, mk, sk, zk);
-        quantise_row<D>(xv, mv, sv, zv);
+        row_codes(xk, odd ? sz2 : sz, odd ? rs2 : rs, mk);
+        row_codes(xv, odd ? sz : sz2, odd ? rs : rs2, mv);
         if (valid) {
             s_k[(word >> 2) * 256 + r * 4 + (word & 3)] = pack_nibbles(mk);
             uint32_t *dst = reinterpret_cast<uint32_t *>(s_v + r * VS + word * 8);
             dst[0] = pack_bytes(mv[0], mv[1], mv[2], mv[3]);
             dst[1] = pack_bytes(mv[4], mv[5], mv[6], mv[7]);
-            if (word == 0) {
-                s_sz[0][r] = pack_sz(sk, zk);
-                s_sz[1][r] = pack_sz(sv, zv);
-            }
+            if (word < 2) s_sz[word][r] = sz;
         }
     }
     __syncthreads();
     // K units of the covered positions
-    for (int i = threadIdx.x; i < (D / 32) * (r1 - r0); i += blockDim.x) {
-        const int j = i / (r1 - r0), u = j * kRecKeys + r0 + (i - j * (r1 - r0));
-        reinterpret_cast<uint4 *>(rec)[u] = reinterpret_cast<const uint4 *>(s_k)[u];
-    }
+    for (int i = threadIdx.x; i < (D / 32) * kRecKeys; i += blockDim.x)
+        if (i % kRecKeys >= r0 && i % kRecKeys < r1)
+            reinterpret_cast<uint4 *>(rec)[i] = reinterpret_cast<const uint4 *>(s_k)[i];
     // V words: 8 positions of one channel; four channels at a time
     uint32_t *vw = reinterpret_cast<uint32_t *>(rec + rec_v_off(D));
     const int g0 = r0 >> 3, n_g = ((r1 + 7) >> 3) - g0;  // groups of 8 positions that the append touches
@@ -280,30 +293,29 @@ __global__ void kvq_append_kernel(const KvqView c, const __nv_bfloat16 *__restri
     }
 }
 
-// Two values s c + z as bf16 (one rounding: the fp32 product of an 8-bit and a
-// 4-bit significand is exact, the sum is rounded to fp32 and then to bf16 -- off
-// by at most half a bf16 step and 2^-24).
-__device__ __forceinline__ uint32_t held_pair(uint32_t c0, float s0, float z0, uint32_t c1, float s1, float z1) {
-    // a small integer as fp32 by its bits: conversion instructions run at a quarter of the rate
-    const float f0 = __uint_as_float(0x4b000000u | c0) - 8388608.f, f1 = __uint_as_float(0x4b000000u | c1) - 8388608.f;
-    const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(f0, s0, z0), fmaf(f1, s1, z1));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ void unpack_sz(uint32_t w, float &s, float &z) {
-    s = __uint_as_float(w << 16);
-    z = __uint_as_float(w & 0xffff0000u);
+// Elements 2 i and 2 i + 1 of a word as bf16 values s c + z, rounded once.  A code in the
+// low bits of 128 (ulp 1) is 128 + c: one mask-and-or, and an exact subtraction.
+__device__ __forceinline__ uint32_t held_pair(uint32_t w, int i, uint32_t s2, uint32_t z2) {
+    uint32_t c2, y;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(c2) : "r"(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u), "r"(0xc300c300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(c2), "r"(s2), "r"(z2));
+    return y;
 }
 
 // The last n positions as bf16 [B][n][Hkv][D]; rows before position 0 are 0.
-// One CTA per record; K: a thread turns one word into 8 channels of a row; V:
-// a thread turns one unit pair (two channels, 32 positions) into 32 stores of a
-// channel pair, so a warp's store covers 128 consecutive bytes of a row.
+// One CTA per record; K: a thread turns one word into 8 channels of a row; V: a thread turns
+// 8 positions of 4 channels (a word each) into 8 stores of 8 bytes, four neighbouring
+// threads take the words of one unit, so a warp's loads share units and its store covers
+// 64 consecutive bytes of 4 rows.
+constexpr int kReadThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kReadThreads)
     kvq_read_kernel(const KvqView c, int n, __nv_bfloat16 *__restrict__ ko, __nv_bfloat16 *__restrict__ vo,
                     int32_t *__restrict__ err) {
-    __shared__ float s_s[2][kRecKeys], s_z[2][kRecKeys];
+    // K: (s, z) of a row; V: s of two neighbouring rows, z of the same two
+    __shared__ uint32_t s_k[kRecKeys];
+    __shared__ uint2 s_v[kRecKeys / 2];
     pdl_wait();
     pdl_launch_dependents();
     const int b = blockIdx.y / c.n_kv_heads, h = blockIdx.y - b * c.n_kv_heads;
@@ -331,35 +343,59 @@ __global__ void __launch_bounds__(128)
         }
         return;
     }
-    for (int i = threadIdx.x; i < 2 * kRecKeys; i += blockDim.x) {
-        const int is_v = i / kRecKeys, r = i - is_v * kRecKeys;
-        const uint32_t w = reinterpret_cast<const uint32_t *>(rec + (is_v ? rec_vs_off(D) : rec_ks_off(D)))[r];
-        unpack_sz(w, s_s[is_v][r], s_z[is_v][r]);
+    // every load of the record before the first use
+    constexpr int NK = kRecKeys * (D / 8) / kReadThreads, NV = 2 * D / kReadThreads;
+    static_assert(NK * kReadThreads == kRecKeys * (D / 8) && NV * kReadThreads == 2 * D, "whole rounds");
+    const auto k_row = [&](int j) { return (int)(threadIdx.x + j * kReadThreads) / (D / 8); };
+    const auto v_group = [&](int j) { return (int)(threadIdx.x + j * kReadThreads) / D * 4 + (int)(threadIdx.x & 3); };
+    const int wd = threadIdx.x % (D / 8);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(rec), *vw = words + rec_v_off(D) / 4;
+    uint32_t kw[NK], w[NV][4];
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+        if (k_row(j) >= r0 && k_row(j) < r1) kw[j] = __ldg(words + (wd >> 2) * 256 + k_row(j) * 4 + (wd & 3));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int g = v_group(j), ch = (int)(threadIdx.x + j * kReadThreads) % D & ~3;
+        if (8 * g < r1 && 8 * g + 8 > r0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[j][i] = __ldg(vw + ((g >> 2) * D + ch + i) * 4 + (g & 3));
+        }
+    }
+    if (threadIdx.x < kRecKeys) {
+        s_k[threadIdx.x] = __ldg(words + rec_ks_off(D) / 4 + threadIdx.x);
+    } else if (threadIdx.x < 3 * kRecKeys / 2) {
+        const int i = threadIdx.x - kRecKeys;
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(rec + rec_vs_off(D)) + i);
+        s_v[i] = make_uint2(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632));
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (r1 - r0) * (D / 8); i += blockDim.x) {
-        const int r = r0 + i / (D / 8), wd = i - i / (D / 8) * (D / 8);
-        const uint32_t w = reinterpret_cast<const uint32_t *>(rec)[(wd >> 2) * 256 + r * 4 + (wd & 3)];
-        const float s = s_s[0][r], z = s_z[0][r];
-        uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = held_pair((w >> nib_bit(2 * k)) & 15u, s, z, (w >> nib_bit(2 * k + 1)) & 15u, s, z);
-        reinterpret_cast<uint4 *>(ko + out_row(r))[wd] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < NK; ++j) {
+        const int r = k_row(j);
+        if (r < r0 || r >= r1) continue;
+        const uint32_t sz = s_k[r], s2 = __byte_perm(sz, sz, 0x1010), z2 = __byte_perm(sz, sz, 0x3232);
+        reinterpret_cast<uint4 *>(ko + out_row(r))[wd] = make_uint4(
+            held_pair(kw[j], 0, s2, z2), held_pair(kw[j], 1, s2, z2), held_pair(kw[j], 2, s2, z2), held_pair(kw[j], 3, s2, z2));
     }
-    const uint4 *vu = reinterpret_cast<const uint4 *>(rec + rec_v_off(D));
-    for (int i = threadIdx.x; i < D; i += blockDim.x) {
-        const int half = i / (D / 2), ch = 2 * (i - half * (D / 2));
-        if (32 * half >= r1 || 32 * half + 32 <= r0) continue;
-        const uint4 ua = vu[half * D + ch], ub = vu[half * D + ch + 1];
-        const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const int r = 32 * half + e;
-            if (r < r0 || r >= r1) continue;
-            const float s = s_s[1][r], z = s_z[1][r];
-            *reinterpret_cast<uint32_t *>(vo + out_row(r) + ch) = held_pair(
-                (wa[e >> 3] >> nib_bit(e)) & 15u, s, z, (wb[e >> 3] >> nib_bit(e)) & 15u, s, z);
+    for (int j = 0; j < NV; ++j) {  // D / 4 channel quads x 8 groups of positions
+        const int g = v_group(j), ch = (int)(threadIdx.x + j * kReadThreads) % D & ~3;
+        if (8 * g >= r1 || 8 * g + 8 <= r0) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint2 sz = s_v[4 * g + k];  // rows 8 g + 2 k and the next
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = held_pair(w[j][i], k, sz.x, sz.y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * g + 2 * k + e;
+                if (r < r0 || r >= r1) continue;
+                const unsigned sel = e ? 0x7632 : 0x5410;
+                *reinterpret_cast<uint2 *>(vo + out_row(r) + ch) =
+                    make_uint2(__byte_perm(y[0], y[1], sel), __byte_perm(y[2], y[3], sel));
+            }
         }
     }
 }
@@ -369,7 +405,7 @@ __global__ void __launch_bounds__(128)
 cudaError_t launch_kvq_append(const KvqView &c, const void *k_new, const void *v_new, int n_new, int32_t *err,
                               cudaStream_t stream) {
     const dim3 grid((unsigned)(((int64_t)n_new + kRecKeys - 2) / kRecKeys + 1), (unsigned)(c.batch * c.n_kv_heads));
-    const int warps = n_new >= 8 ? 8 : 4;  // a warp per token; four also share out a single token's V words
+    const int warps = n_new >= 8 ? kAppendWarps : 4;  // four also share out a single token's V words
     const auto *k = static_cast<const __nv_bfloat16 *>(k_new), *v = static_cast<const __nv_bfloat16 *>(v_new);
     const dim3 block(32 * warps);
     switch (c.head_dim) {
@@ -384,9 +420,9 @@ cudaError_t launch_kvq_read(const KvqView &c, int n, void *k_out, void *v_out, i
     const dim3 grid((unsigned)(((int64_t)n + kRecKeys - 2) / kRecKeys + 1), (unsigned)(c.batch * c.n_kv_heads));
     auto *k = static_cast<__nv_bfloat16 *>(k_out), *v = static_cast<__nv_bfloat16 *>(v_out);
     switch (c.head_dim) {
-        case 64: return launch_pdl(kvq_read_kernel<64>, grid, dim3(128), 0, stream, c, n, k, v, err);
-        case 128: return launch_pdl(kvq_read_kernel<128>, grid, dim3(128), 0, stream, c, n, k, v, err);
-        case 256: return launch_pdl(kvq_read_kernel<256>, grid, dim3(128), 0, stream, c, n, k, v, err);
+        case 64: return launch_pdl(kvq_read_kernel<64>, grid, dim3(kReadThreads), 0, stream, c, n, k, v, err);
+        case 128: return launch_pdl(kvq_read_kernel<128>, grid, dim3(kReadThreads), 0, stream, c, n, k, v, err);
+        case 256: return launch_pdl(kvq_read_kernel<256>, grid, dim3(kReadThreads), 0, stream, c, n, k, v, err);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -2,6 +2,7 @@
 // encoding and kernel launches.  Declarations and contracts: include/wm_api.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
