@@ -657,6 +657,12 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
             return __uint_as_float((uint32_t)(127 + ex) << 23);
         };
 
+        // This thread's addresses: its keys' constants, its row of P' (its first 16-byte unit,
+        // swizzled; with 16 rows per warp the second is the neighbour in a pair).
+        const uint32_t c_at = s_const + kt * 16, z_at = s_zr + kt * 4;
+        const uint32_t swizzle = C::PT_ROW == 128 ? kt & 7 : C::PT_ROW == 64 ? (kt >> 1) & 3 : (kt >> 2) & 1;
+        const uint32_t p_at = sPT + kt * C::PT_ROW + ((r0 / 8 ^ swizzle) << 4);
+
         KvqPart q;
         int g = 0, part = 0;
         bool have = walk.next(p.c, q);
@@ -734,25 +740,31 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 tc::fence_before_sync();
 
                 // t - m of every row
+                const uint32_t held = 2 * gt & 3;
+                uint64_t a2[2], b2[2], ls2[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint4 kc = ld_shared_v4(s_const + (((2 * gt + j) & 3) * 128 + kt) * 16);
+                    const uint4 kc = ld_shared_v4(c_at + (held + j) * 2048);
                     const float a = __uint_as_float(kc.x) * f, bz = __uint_as_float(kc.y) * f;
-                    const uint64_t a2 = pack2(a, a), b2 = pack2(bz, bz);
-                    const uint64_t ls2 = pack2(__uint_as_float(kc.z), __uint_as_float(kc.z));
+                    a2[j] = pack2(a, a);
+                    b2[j] = pack2(bz, bz);
+                    ls2[j] = pack2(__uint_as_float(kc.z), __uint_as_float(kc.z));
+                }
 #pragma unroll
-                    for (int i = 0; i < HR; i += 4) {
-                        const ulonglong2 z4 = ld_shared_pairs(zq + 4 * i), m4 = ld_shared_pairs(nm + 4 * i);
+                for (int i = 0; i < HR; i += 4) {
+                    const ulonglong2 z4 = ld_shared_pairs(zq + 4 * i), m4 = ld_shared_pairs(nm + 4 * i);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         float *x = s[j] + i;
-                        unpack2(fma2(pack2(x[0], x[1]), a2, fma2(z4.x, b2, add2(ls2, m4.x))), x[0], x[1]);
-                        unpack2(fma2(pack2(x[2], x[3]), a2, fma2(z4.y, b2, add2(ls2, m4.y))), x[2], x[3]);
+                        unpack2(fma2(pack2(x[0], x[1]), a2[j], fma2(z4.x, b2[j], add2(ls2[j], m4.x))), x[0], x[1]);
+                        unpack2(fma2(pack2(x[2], x[3]), a2[j], fma2(z4.y, b2[j], add2(ls2[j], m4.y))), x[2], x[3]);
                     }
                 }
                 float inv[2], zr[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    inv[j] = ld_shared_f32(s_const + (((2 * gt + j) & 3) * 128 + kt) * 16 + 12);
-                    zr[j] = ld_shared_f32(s_zr + (((2 * gt + j) & 3) * 128 + kt) * 4);
+                    inv[j] = ld_shared_f32(c_at + (held + j) * 2048 + 12);
+                    zr[j] = ld_shared_f32(z_at + (held + j) * 512);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_sfree);  // S and the constants are read
@@ -780,25 +792,29 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                         if (lane == 0) st_shared_f32(s_red + (4 * (r0 + i) + q4) * 4, mx);
                     }
                     named_bar_sync(2 + grp, 128);
-                    // by how much row i's maximum goes up
-                    const auto up = [&](int i) -> float {
-                        const float4 x = ld_shared_f4(s_red + 16 * (r0 + i));
-                        const float mx = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) - kKvqOff;
-                        return t > 0 ? fmaxf(mx, 0.f) : mx == -CUDART_INF_F ? 0.f : mx;
-                    };
+                    // Lane i holds by how much the maximum of row i of HR goes up; the others ask it.
+                    const float4 m4 = ld_shared_f4(s_red + 16 * (r0 + lane % HR));
+                    const float mx = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)) - kKvqOff;
+                    const float up = t > 0 ? fmaxf(mx, 0.f) : mx == -CUDART_INF_F ? 0.f : mx, down = ex2(-up);
+                    if (q4 == 0 && lane < HR) st_shared_f32(nm + 4 * lane, ld_shared_f32(nm + 4 * lane) - up);
 #pragma unroll
                     for (int i = 0; i < HR; ++i) {
-                        const float d = up(i);
+                        const float d = __shfl_sync(0xffffffffu, up, i);
                         s[0][i] -= d;
                         s[1][i] -= d;
                     }
-                    if (q4 == 0 && lane < HR) st_shared_f32(nm + 4 * lane, ld_shared_f32(nm + 4 * lane) - up(lane));
                     if (t > 0) {
 #pragma unroll
-                        for (int i = 0; i < HR / 2; ++i) {
-                            const uint64_t al = pack2(ex2(-up(2 * i)), ex2(-up(2 * i + 1)));
-                            l2[i] = mul2(l2[i], al);
-                            z2[i] = mul2(z2[i], al);
+                        for (int j = 0; j < HR / 8; ++j) {
+                            float al[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) al[i] = __shfl_sync(0xffffffffu, down, 8 * j + i);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint64_t al2 = pack2(al[2 * i], al[2 * i + 1]);
+                                l2[4 * j + i] = mul2(l2[4 * j + i], al2);
+                                z2[4 * j + i] = mul2(z2[4 * j + i], al2);
+                            }
                         }
                     }
                     if ((LONG ? t % kKvqChain : t) > 0) {
@@ -806,18 +822,23 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                         wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
                         __syncwarp();
                         tc::fence_after_sync();
+                        // (unrolled, these loops cost the common path registers: 2 x 1M 696 us for 671)
+#pragma unroll 1
+                        for (int j = 0; j < HR / 8; ++j) {
+                            float al[8];
 #pragma unroll
-                        for (int c = 0; c < NC; ++c)
-#pragma unroll
-                            for (int j = 0; j < HR / 8; ++j) {
+                            for (int i = 0; i < 8; ++i) al[i] = __shfl_sync(0xffffffffu, down, 8 * j + i);
+#pragma unroll 1
+                            for (int c = 0; c < NC; ++c) {
                                 const uint32_t at = tmem + lane_off + C::O_COL + c * NR + r0 + 8 * j;
                                 float v8[8];
                                 tc::ld_32x32b_x8(at, v8);
                                 tc::wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v8[i] *= ex2(-up(8 * j + i));
+                                for (int i = 0; i < 8; ++i) v8[i] *= al[i];
                                 tc::st_32x32b_x8(at, v8);
                             }
+                        }
                         tc::wait_st();
                     }
                     named_bar_sync(2 + grp, 128);  // the new maxima are visible, red is free
@@ -828,7 +849,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint64_t inv2 = pack2(inv[j], inv[j]), zr2 = pack2(zr[j], zr[j]);
-                    const uint32_t pt = sPT + (gt % NPB) * C::PB_BYTES + j * C::PT_BYTES;
+                    const uint32_t pt = p_at + (gt % NPB) * C::PB_BYTES;
 #pragma unroll
                     for (int i0 = 0; i0 < HR; i0 += 8) {
                         uint32_t w[4];
@@ -842,11 +863,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                             const __half2 hv = __floats2half2_rn(x, y);
                             w[k] = *reinterpret_cast<const uint32_t *>(&hv);
                         }
-                        const int chunk = (r0 + i0) / 8;
-                        const uint32_t phys = C::PT_ROW == 128 ? (uint32_t)(chunk ^ (kt & 7))
-                                              : C::PT_ROW == 64 ? (uint32_t)(chunk ^ ((kt >> 1) & 3))
-                                                                : (uint32_t)(chunk ^ ((kt >> 2) & 1));
-                        st_shared_v4(pt + (uint32_t)kt * C::PT_ROW + (phys << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                        st_shared_v4((pt ^ (2 * i0)) + j * C::PT_BYTES, make_uint4(w[0], w[1], w[2], w[3]));
                     }
                 }
                 fence_proxy_async_smem();
