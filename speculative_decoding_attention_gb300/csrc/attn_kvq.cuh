@@ -32,7 +32,7 @@
 // rounds by 0.17%.  Every
 // kKvqChain tiles the softmax warps therefore add O to fp32 sums of their own (rounded, in
 // the part's slot of the workspace, which each thread alone touches) and the products start
-// O anew.  (LONG: the kernel for capacities at which a part can be longer than that.)
+// O anew.
 //
 // Each CTA takes one run of the batch's tiles (kvq_schedule), cut into parts at
 // (sequence, KV head) borders; every role counts tiles across parts, so no
@@ -250,7 +250,7 @@ __device__ __forceinline__ bool kvq_wait_slow(uint32_t bar, uint32_t parity, uin
     return false;
 }
 
-template <int D, int NR, bool LONG>
+template <int D, int NR>
 __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(const KvqAttnParams p) {
     using C = KvqCfg<D, NR>;
     constexpr int TK = kKvqTile, NC = C::NC, HR = C::HR, NSW = C::NSW, ND = C::ND, NST = C::NST, NPB = C::NPB;
@@ -466,8 +466,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk) {  // 16 keys each
                                 const uint64_t bp = pb + ((kk * 2 * C::PT_ATOM) >> 4);
-                                mma_f16_ts(d, a + 8 * kk, bp, id_pv,
-                                           (LONG ? t % kKvqChain : t) > 0 || j > 0 || kk > 0);
+                                mma_f16_ts(d, a + 8 * kk, bp, id_pv, t % kKvqChain > 0 || j > 0 || kk > 0);
                                 mma_f16_ts(d, tmem + C::E_COL, bp, id_pv, 1u);
                             }
                             tc::commit(bar_afree + 8 * (C::KS + slot));
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                 const int gt = g + t;
                 const int key0 = key_first + t * TK;
 
-                if (LONG && __builtin_expect(t > 0 && t % kKvqChain == 0, 0)) {
+                if (__builtin_expect(t > 0 && t % kKvqChain == 0, 0)) {
                     // take O over (it is at the maxima of the last tile, which are still the present ones)
                     wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
                     __syncwarp();
@@ -817,7 +816,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                             }
                         }
                     }
-                    if ((LONG ? t % kKvqChain : t) > 0) {
+                    if (t % kKvqChain > 0) {
                         // O holds tiles at the old maxima
                         wait(bar_odone + 8 * ((gt - 1) % NPB), (gt - 1) / NPB);
                         __syncwarp();
@@ -920,7 +919,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
                     tc::wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o8[i] = fmaf(o8[i], 16777216.f, z8[i]);
-                    if (LONG && __builtin_expect(n > kKvqChain, 0)) add_over(c, j, (n - 1) / kKvqChain, o8);
+                    if (__builtin_expect(n > kKvqChain, 0)) add_over(c, j, (n - 1) / kKvqChain, o8);
                     const int d = c * 128 + kt;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -951,7 +950,7 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     }
 }
 
-template <int D, int NR, bool LONG>
+template <int D, int NR>
 cudaError_t launch_kvq_attn_nr(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
     constexpr int smem = KvqCfg<D, NR>::TOTAL;
     static bool configured[64] = {};
@@ -960,20 +959,20 @@ cudaError_t launch_kvq_attn_nr(const KvqAttnParams &p, int n_cta, cudaStream_t s
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    return launch_pdl(kvq_attn_kernel<D, NR, LONG>, dim3(n_cta), dim3(KvqCfg<D, NR>::THREADS), smem, stream, p);
+    return launch_pdl(kvq_attn_kernel<D, NR>, dim3(n_cta), dim3(KvqCfg<D, NR>::THREADS), smem, stream, p);
 }
 
-template <int D, bool LONG>
+template <int D>
 cudaError_t launch_kvq_attn_d(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
     switch ((p.rows + 15) / 16) {
-        case 1: return launch_kvq_attn_nr<D, 16, LONG>(p, n_cta, stream);
-        case 2: return launch_kvq_attn_nr<D, 32, LONG>(p, n_cta, stream);
-        case 3: return launch_kvq_attn_nr<D, 48, LONG>(p, n_cta, stream);
-        case 4: return launch_kvq_attn_nr<D, 64, LONG>(p, n_cta, stream);
+        case 1: return launch_kvq_attn_nr<D, 16>(p, n_cta, stream);
+        case 2: return launch_kvq_attn_nr<D, 32>(p, n_cta, stream);
+        case 3: return launch_kvq_attn_nr<D, 48>(p, n_cta, stream);
+        case 4: return launch_kvq_attn_nr<D, 64>(p, n_cta, stream);
         default: return cudaErrorInvalidValue;
     }
 }

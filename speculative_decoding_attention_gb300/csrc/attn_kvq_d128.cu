@@ -4,7 +4,7 @@
 namespace wm {
 
 cudaError_t launch_kvq_attn_d128(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
-    return launch_kvq_attn_d<128, false>(p, n_cta, stream);
+    return launch_kvq_attn_d<128>(p, n_cta, stream);
 }
 
 }  // namespace wm

@@ -4,7 +4,7 @@
 namespace wm {
 
 cudaError_t launch_kvq_attn_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
-    return launch_kvq_attn_d<256, false>(p, n_cta, stream);
+    return launch_kvq_attn_d<256>(p, n_cta, stream);
 }
 
 }  // namespace wm

@@ -85,11 +85,11 @@ struct KvqAttnParams {
 };
 
 constexpr int kKvqTile = 256;  // positions per attention tile: two sub-tiles of two records
-// Tiles whose products one accumulator takes up (attn_kvq.cuh has the drift of long chains):
-// kKvqWhole where no part can be longer, else kKvqChain.  The error of an average over a
-// million random positions, of which bf16's rounding of the output is 0.16%: 0.171%
-// at 32 tiles, 0.189% at 48, 0.215% at 64 and 0.72% at 432 (head_dim 128).
-constexpr int kKvqWhole = 64, kKvqChain = 32;
+// Tiles whose products one accumulator takes up (attn_kvq.cuh has the drift of long chains).
+// The error of an average over a million random positions, of which bf16's rounding of the
+// output is 0.16%: 0.171% at 32 tiles, 0.189% at 48, 0.215% at 64 and 0.72% at 432 (head_dim
+// 128); 64 are 2% faster than 32 where a CTA has 432.
+constexpr int kKvqChain = 32;
 
 __device__ __forceinline__ int kvq_tiles(const KvqView &c, int b) {
     return (int)((kvq_len(c, b) + kKvqTile - 1) / kKvqTile);
@@ -248,11 +248,8 @@ struct KvqWalk {
 
 // The attention grid per head_dim (attn_kvq_d<D>.cu), and the merge of its parts.
 cudaError_t launch_kvq_attn_d64(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
-cudaError_t launch_kvq_attn_long_d64(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_attn_d128(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
-cudaError_t launch_kvq_attn_long_d128(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_attn_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
-cudaError_t launch_kvq_attn_long_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_merge(const KvqAttnParams &p, cudaStream_t stream);
 
 cudaError_t launch_kvq_append(const KvqView &c, const void *k_new, const void *v_new, int n_new, int32_t *err,

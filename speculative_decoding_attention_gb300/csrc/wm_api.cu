@@ -2,7 +2,6 @@
 // encoding and kernel launches.  Declarations and contracts: include/wm_api.h.
 #include <cudaTypedefs.h>
 
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -865,13 +864,9 @@ wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32
     std::memset(&p, 0, sizeof p);
     p.c = kvq_view(kv);
     const int64_t units = (int64_t)kv->batch * kv->n_kv_heads;
-    const int64_t tiles = (p.c.capacity + kKvqTile - 1) / kKvqTile;
-    if (units * tiles > (int64_t)1 << 30) return WM_ERR_UNSUPPORTED;  // tile counts stay within 32 bits
+    // tile counts stay within 32 bits
+    if (units * ((p.c.capacity + kKvqTile - 1) / kKvqTile) > (int64_t)1 << 30) return WM_ERR_UNSUPPORTED;
     const int n_cta = kvq_ctas();
-    // Tiles of the longest part that the capacity can give: short enough, and the kernel without
-    // the code that takes accumulators over runs (1M positions at head_dim 256, 54 tiles a part:
-    // 148 us, with it 159; 64 sequences at head_dim 64: 56 and 62).
-    const bool whole = std::min(tiles, (units * tiles + n_cta - 1) / n_cta) <= kKvqWhole;
     const KvqLayout l = kvq_layout(n_cta, units, (int)rows, kv->head_dim, kv->batch);
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256)) return WM_ERR_WORKSPACE;
     char *w = static_cast<char *>(workspace);
@@ -891,10 +886,9 @@ wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32
     p.wait_limit = t_wait_limit;
     p.stall_tile = t_stall_tile;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto launch = kv->head_dim == 64    ? (whole ? launch_kvq_attn_d64 : launch_kvq_attn_long_d64)
-                        : kv->head_dim == 128 ? (whole ? launch_kvq_attn_d128 : launch_kvq_attn_long_d128)
-                                              : (whole ? launch_kvq_attn_d256 : launch_kvq_attn_long_d256);
-    const cudaError_t e = launch(p, n_cta, st);
+    const cudaError_t e = kv->head_dim == 64    ? launch_kvq_attn_d64(p, n_cta, st)
+                          : kv->head_dim == 128 ? launch_kvq_attn_d128(p, n_cta, st)
+                                                : launch_kvq_attn_d256(p, n_cta, st);
     if (e != cudaSuccess) return WM_ERR_CUDA;
     return launch_status(launch_kvq_merge(p, st));
 }
