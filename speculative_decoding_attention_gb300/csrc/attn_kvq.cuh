@@ -60,19 +60,21 @@ namespace wm {
 constexpr float kKvqOff = 7.f;       // the running maximum sits at 2^7 in P': fp16 keeps 11 bits down to 2^-21 of it
 constexpr float kKvqRaise = 8.f;     // raise the maximum only past 2^8 (P' <= 2^15, fp16 holds up to 65504)
 
-template <int D_, int NR_>
+// NR: the MMA's N, a multiple of 16; LIVE: rows that have softmax warps (nothing reads the
+// columns of P', S and O past them).
+template <int D_, int NR_, int LIVE_>
 struct KvqCfg {
-    static constexpr int D = D_, NR = NR_;
+    static constexpr int D = D_, NR = NR_, LIVE = LIVE_;
     static constexpr int REC = rec_bytes(D);
     static constexpr int STAGE = 2 * REC;               // a sub-tile of 128 keys
     static constexpr int NC = D == 256 ? 2 : 1;         // 128-channel chunks
     static constexpr int KU = D == 64 ? 2 : 4;          // 16-byte units per key and chunk
     // Rows per softmax warp and converting warps.  More warps hide more latency, fewer leave
     // more registers to each and repeat less per-key work; measured in us, chosen form first:
-    // up to 16 rows at head_dim 128 (ragged batch of 2.4 GB) 16 warps 463, 12 531, 8 549; 32
-    // rows at head_dim 256 (1M positions) 4 warps 140, 8 158; at 128 (128K) 4 warps 37.2, 8
-    // 38.4, and 16 rows per softmax warp instead of 8 42; 48 rows (2 x 1M) 16 rows per
-    // softmax warp and 4 converting 662, 8 and 4 996, 16 and 8 963.
+    // up to 16 rows at head_dim 128 (ragged batch of 2.4 GB) 16 converting warps 515, 8 563, 4
+    // 644; at 64 (64 short sequences) 8 warps 54, 4 55, 16 61; 32 rows at 256 (1M positions)
+    // 4 warps 137, 8 144 with peaked keys, 134 and 125 without; at 128 (128K) 4 and 8 36; 48 rows
+    // (2 x 1M) 16 rows per softmax warp and 4 converting 674, 8 converting 907.
     static constexpr int HR = NR <= 32 ? 8 : 16;
     static constexpr int ND = NR == 16 ? (D == 128 ? 16 : 8) : 4;
     static constexpr int KG = ND == 16 ? 2 : 1, VG = KG;  // warp groups for K and V
@@ -80,7 +82,7 @@ struct KvqCfg {
     // follow every use of it).
     static_assert(KG == 1 || NC == 1, "a group owns its slots");
     static_assert(HR == 8 || HR == 16, "rows per softmax warp");
-    static constexpr int NSW = 4 * (NR / HR);           // softmax warps
+    static constexpr int NSW = 4 * (LIVE / HR);         // softmax warps
     static constexpr int W_D = 3, W_S = 3 + ND;         // first converting and first softmax warp
     static constexpr int THREADS = 32 * (W_S + NSW);
     // tensor memory: K and V code slots of 64 columns, the constant -8 (8 columns), S of two sub-tiles, O
@@ -250,9 +252,9 @@ __device__ __forceinline__ bool kvq_wait_slow(uint32_t bar, uint32_t parity, uin
     return false;
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(const KvqAttnParams p) {
-    using C = KvqCfg<D, NR>;
+template <int D, int NR, int LIVE>
+__global__ void __launch_bounds__(KvqCfg<D, NR, LIVE>::THREADS, 1) kvq_attn_kernel(const KvqAttnParams p) {
+    using C = KvqCfg<D, NR, LIVE>;
     constexpr int TK = kKvqTile, NC = C::NC, HR = C::HR, NSW = C::NSW, ND = C::ND, NST = C::NST, NPB = C::NPB;
 
     extern __shared__ uint8_t smem_raw[];
@@ -950,27 +952,33 @@ __global__ void __launch_bounds__(KvqCfg<D, NR>::THREADS, 1) kvq_attn_kernel(con
     }
 }
 
-template <int D, int NR>
+template <int D, int NR, int LIVE = NR>
 cudaError_t launch_kvq_attn_nr(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
-    constexpr int smem = KvqCfg<D, NR>::TOTAL;
+    constexpr int smem = KvqCfg<D, NR, LIVE>::TOTAL;
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kvq_attn_kernel<D, NR, LIVE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    return launch_pdl(kvq_attn_kernel<D, NR>, dim3(n_cta), dim3(KvqCfg<D, NR>::THREADS), smem, stream, p);
+    return launch_pdl(kvq_attn_kernel<D, NR, LIVE>, dim3(n_cta), dim3(KvqCfg<D, NR, LIVE>::THREADS), smem, stream, p);
 }
 
 template <int D>
 cudaError_t launch_kvq_attn_d(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
+    // Rows past the last query's have no softmax warps where that frees a group of them: single
+    // tokens of 16 sequences of 32K-64K, 8 rows of 128, 82 us (with warps for 16 rows 94); one
+    // sequence of 512K, 24 rows of 128, 82 (with warps for 32 rows 90).
+    if (p.rows <= 8) return launch_kvq_attn_nr<D, 16, 8>(p, n_cta, stream);
     switch ((p.rows + 15) / 16) {
         case 1: return launch_kvq_attn_nr<D, 16>(p, n_cta, stream);
-        case 2: return launch_kvq_attn_nr<D, 32>(p, n_cta, stream);
+        case 2:
+            return p.rows <= 24 ? launch_kvq_attn_nr<D, 32, 24>(p, n_cta, stream)
+                                : launch_kvq_attn_nr<D, 32>(p, n_cta, stream);
         case 3: return launch_kvq_attn_nr<D, 48>(p, n_cta, stream);
         case 4: return launch_kvq_attn_nr<D, 64>(p, n_cta, stream);
         default: return cudaErrorInvalidValue;
