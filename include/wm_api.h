@@ -14,6 +14,11 @@
  *   - the split-KV partial results of either are combined by a log-sum-exp
  *     merge                                            -> wm_lse_merge.
  *
+ * Beside the bf16 cache there is a full-context cache held in 4 bits
+ * (wm_kvq_append, wm_kvq_read, wm_verify_attn_kvq), and the step's last part, the
+ * acceptance of the drafted tokens, whose new lengths wm_ring_rollback takes
+ * (wm_spec_accept).
+ *
  * Conventions shared by every entry point
  *   - Element types: K, V, q and out are bf16 (IEEE binary16-brain, 2 bytes);
  *     lse and split partials are fp32; positions/lengths int64; tags and page
@@ -389,9 +394,10 @@ size_t wm_workspace_size(int32_t op, int32_t batch, int32_t n_kv_heads, int32_t 
  *       multiple of 64; block_table [batch][max_pages] int32 as for wm_kv
  *   seq_lens [batch] int64: number of valid positions of each sequence.
  * A sequence holds at most INT32_MAX - 512 positions (n_cap, or max_pages *
- * page_size; WM_ERR_UNSUPPORTED otherwise).  data must be 16-byte aligned.  No initial contents are needed: positions at or
- * past seq_lens[b] are never used, whatever their bytes.  A page that an append
- * writes must belong to one sequence.
+ * page_size; WM_ERR_UNSUPPORTED otherwise).  data must be 16-byte aligned.  No
+ * initial contents are needed: positions at or past seq_lens[b] are never used,
+ * whatever their bytes.  A page that an append writes must be in one place of one
+ * block table (sequences may share pages that are only read).
  */
 typedef struct wm_kvq {
     void *data;
@@ -420,10 +426,10 @@ size_t wm_kvq_record_bytes(int32_t head_dim);
  *   z = min x_d;  s = (max x_d - z) / 15 rounded to bf16 (nearest even);
  *   c_d = min(15, max(0, rint(t_d / s))), t_d = x_d - z in fp32, the quotient
  *   exact and ties to even;  c_d = 0 if s = 0.
- * The range and its fifteenth are as doubles give them.  A row that holds a NaN or an infinity
- * gets s = z = NaN and attention over it gives NaN.  Other positions of the
- * records keep their codes.  A seq_lens[b] that is negative or beyond the capacity records
- * WM_DEVERR_BAD_LENGTH and nothing is written for b; a block-table entry
+ * The range and its fifteenth are as doubles give them.  A row that holds a NaN or an
+ * infinity gets s = z = NaN and attention over it gives NaN.  Other positions of the
+ * records keep their codes.  A seq_lens[b] that is negative or beyond the capacity
+ * records WM_DEVERR_BAD_LENGTH and nothing is written for b; a block-table entry
  * outside the pool records WM_DEVERR_BAD_PAGE and its positions are skipped.
  */
 wm_status wm_kvq_append(const wm_kvq *kv, const void *k_new, const void *v_new, int32_t n_new, void *stream);
@@ -449,6 +455,9 @@ wm_status wm_kvq_read(const wm_kvq *kv, int32_t n, void *k_out, void *v_out, voi
  * The work is split on the device from the actual lengths: one CTA per SM takes
  * an equal run of the batch's 256-position tiles.  Two launches.  Results do
  * not depend on what else runs: repeated calls are bit-identical.
+ * A query before position 0 sees no key: out 0, lse -INFINITY.  A length outside
+ * [0, capacity] records WM_DEVERR_BAD_LENGTH and is clamped; a block-table entry
+ * outside the pool records WM_DEVERR_BAD_PAGE and page 0 is read in its place.
  * At most 64 rows (n_q * n_q_heads / n_kv_heads) per KV head and 2^30 tiles
  * (batch * n_kv_heads * ceil(capacity / 256)); WM_ERR_UNSUPPORTED beyond.
  */
@@ -491,11 +500,13 @@ size_t wm_kvq_workspace_size(int32_t batch, int32_t n_kv_heads, int32_t n_q_head
  *                 what wm_ring_rollback takes
  * Greedy verification: pass one-hot target rows.  Probabilities need not sum
  * to 1; a NaN or negative one counts as 0, one above 1 as 1, and the same holds for the u's.
- * The sums carry about 48 bits, in an order that the shapes alone fix.
+ * The sums carry about 48 bits, in an order that the shapes and the device's number of
+ * SMs fix: the same inputs give the same tokens on every call.
  * n_draft[b] outside [0, k] records WM_DEVERR_BAD_LENGTH and is clamped; a
  * draft outside [0, vocab) records WM_DEVERR_BAD_TOKEN and is refused; a
  * row without weight records WM_DEVERR_BAD_PROB and gives token -1.
- * k >= 1, batch <= 65535.  One launch, no workspace.  The outputs must not
+ * k >= 1, batch <= 65535; vocab <= 2^30 and k <= 2^20 (WM_ERR_UNSUPPORTED beyond).
+ * One launch, no workspace.  The outputs must not
  * overlap the inputs otherwise.
  */
 wm_status wm_spec_accept(const float *target_probs, const float *draft_probs, const int32_t *draft_tokens,
