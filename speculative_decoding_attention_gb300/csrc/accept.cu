@@ -17,8 +17,11 @@
 // one, from L2), then the entry.  The other CTAs leave as soon as every total has
 // been read.  One launch, no workspace, no atomics, so the same inputs give the
 // same token in any launch.
-// What bounds it: HBM for a large batch; for one sequence the chain of dependent
-// loads (draft, its probabilities, the row, the search).
+// A row is summed in one pass, two entries per instruction (6 instructions an entry without
+// a draft row; one at a time, with checks in the loop, 31 took 50 us where this takes 32).
+// What bounds it: HBM for a large batch (256 rows of 131072 entries, 134 MB: 32 us, of
+// which the stream is 20 at HBM's rate); for one sequence the chain of dependent loads
+// (draft, its probabilities, the row, the search), 9 us.
 #include <cooperative_groups.h>
 
 #include "kvq.cuh"
@@ -32,7 +35,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kAcceptThreads = 512;
 constexpr int kAcceptWarps = kAcceptThreads / 32;
-constexpr int kLoads = 4;  // entries per lane whose loads are in flight together
+// Loads per lane in flight together, and CTAs per SM, which bound the registers: 256 rows of
+// 131072 entries take 32 us; with 8 loads 34.7, with 32 35.5; with 4 CTAs and 8 loads 37, with
+// 3 38.8.
+constexpr int kLoads = 16, kAcceptPerSm = 2;
 
 // hi + lo, hi the nearest float.
 struct Pair {
@@ -135,28 +141,82 @@ __device__ __forceinline__ Pair from(const float2 *x, int lane, int n) {
     return lane < n ? Pair{x[lane].x, x[lane].y} : Pair{};
 }
 
-// Sum of entries [i0, i1) of the row over one warp, on every lane.
-__device__ __forceinline__ Pair run_sum(const Row &row, int i0, int i1, int lane) {
-    Pair acc;
-    for (; i0 < i1; i0 += 32 * kLoads) {
-        float pv[kLoads], qv[kLoads];
+// Sums of two entries' lanes side by side, each as a Pair.
+struct Pairs {
+    uint64_t hi = 0, lo = 0;
+    // a - b in both, rounded once
+    static __device__ __forceinline__ uint64_t minus(uint64_t a, uint64_t b) {
+        return fma2(b, pack2(-1.f, -1.f), a);
+    }
+    __device__ __forceinline__ uint64_t add(uint64_t d) {  // returns the errors
+        const uint64_t s = add2(hi, d), bb = minus(s, hi);
+        const uint64_t e = add2(minus(hi, minus(s, bb)), minus(d, bb));
+        hi = s;
+        return e;
+    }
+    __device__ __forceinline__ Pair sum() const {
+        float h0, h1, l0, l1;
+        unpack2(hi, h0, h1);
+        unpack2(lo, l0, l1);
+        return (Pair{} + Pair{h0, l0}) + (Pair{} + Pair{h1, l1});
+    }
+};
+
+// Adds entries i, i + 32, .. of a lane (L of them, those below i1 if TAIL); p and q point at i.
+template <bool Q, bool TAIL, int L>
+__device__ __forceinline__ void add_block(Pairs &acc, const float *p, const float *q, int i, int i1, int skip) {
+    float pv[L], qv[L];
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int i = i0 + 32 * j + lane;
-            pv[j] = qv[j] = 0.f;
-            if (i < i1) row.load(i, pv[j], qv[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            float d, e;
-            row.weight(pv[j], qv[j], i0 + 32 * j + lane, d, e);
-            acc.add(d, e);
+    for (int j = 0; j < L; ++j) {
+        pv[j] = qv[j] = 0.f;
+        if (!TAIL || i + 32 * j < i1) {
+            pv[j] = __ldg(p + 32 * j);
+            if (Q) qv[j] = __ldg(q + 32 * j);
         }
     }
-    return warp_sum(Pair{} + acc);
+    if (!Q && (unsigned)(skip - i) < 32u * L) {
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (i + 32 * j == skip) pv[j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < L; j += 2) {
+        const uint64_t p2 = pack2(__saturatef(pv[j]), __saturatef(pv[j + 1]));
+        if (Q) {
+            const uint64_t q2 = pack2(__saturatef(qv[j]), __saturatef(qv[j + 1]));
+            const uint64_t d2 = Pairs::minus(p2, q2);
+            float d0, d1, e0, e1;
+            unpack2(d2, d0, d1);
+            unpack2(Pairs::minus(Pairs::minus(p2, d2), q2), e0, e1);  // exact where d > 0
+            if (!(d0 > 0.f)) d0 = e0 = 0.f;
+            if (!(d1 > 0.f)) d1 = e1 = 0.f;
+            acc.lo = add2(acc.lo, add2(acc.add(pack2(d0, d1)), pack2(e0, e1)));
+        } else {
+            acc.lo = add2(acc.lo, acc.add(p2));
+        }
+    }
 }
 
-__global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const AcceptParams P) {
+// Sum of entries [i0, i1) of the row over one warp, on every lane.
+template <bool Q>
+__device__ __forceinline__ Pair run_sum(const Row &row, int i0, int i1, int lane) {
+    constexpr int L = Q ? kLoads / 2 : kLoads;
+    Pairs acc;
+    int i = i0 + lane;
+    const float *p = row.p + i, *q = Q ? row.q + i : nullptr;
+    for (; i - lane + 32 * L <= i1; i += 32 * L, p += 32 * L) {
+        add_block<Q, false, L>(acc, p, q, i, i1, row.skip);
+        if (Q) q += 32 * L;
+    }
+    if (i - lane < i1) add_block<Q, true, L>(acc, p, q, i, i1, row.skip);
+    return warp_sum(acc.sum());
+}
+
+__device__ __forceinline__ Pair run_sum(const Row &row, int i0, int i1, int lane) {
+    return row.q ? run_sum<true>(row, i0, i1, lane) : run_sum<false>(row, i0, i1, lane);
+}
+
+__global__ void __launch_bounds__(kAcceptThreads, kAcceptPerSm) spec_accept_kernel(const AcceptParams P) {
     __shared__ int s_a, s_n, s_x, s_owner;
     __shared__ float2 s_warp[kAcceptWarps], s_sub[kAcceptWarps], s_total[2], s_base, s_t;
     pdl_wait();
@@ -318,11 +378,11 @@ __global__ void __launch_bounds__(kAcceptThreads, 4) spec_accept_kernel(const Ac
 }  // namespace
 
 cudaError_t launch_spec_accept(const AcceptParams &p, int sms, cudaStream_t stream) {
-    // CTAs per sequence: as many as leave every CTA resident at once (four per SM), so
-    // that one sequence is spread as wide as a portable cluster goes and a large
-    // batch pays the fixed cost of a CTA (about as long as 128 KB take) rarely.
+    // CTAs per sequence: as many as leave every CTA resident at once, so that one sequence is
+    // spread as wide as a portable cluster goes and a large batch pays the fixed cost of a
+    // CTA (about as long as 128 KB take) rarely.
     unsigned n = 8;
-    while (n > 1 && (int64_t)p.batch * n > 4ll * sms) n >>= 1;
+    while (n > 1 && (int64_t)p.batch * n > (int64_t)kAcceptPerSm * sms) n >>= 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kAcceptThreads);
     cfg.stream = stream;
