@@ -76,11 +76,13 @@ struct KvqCfg {
     // Rows per softmax warp and converting warps.  More warps hide more latency, fewer leave
     // more registers to each and repeat less per-key work; measured in us, chosen form first:
     // up to 16 rows at head_dim 128 (ragged batch of 2.4 GB) 16 converting warps 515, 8 563, 4
-    // 644; at 64 (64 short sequences) 8 warps 54, 4 55, 16 61; 32 rows at 256 (1M positions)
-    // 4 warps 137, 8 144 with peaked keys, 134 and 125 without; at 128 (128K) 4 and 8 36; 48 rows
-    // (2 x 1M) 16 rows per softmax warp and 4 converting 674, 8 converting 907.
+    // 644; at 64 (64 short sequences) 8 warps 54, 4 55, 16 61; 24 rows at 128 (512K positions)
+    // 8 warps 77, 4 82; at 256 (1M) 8 115, 4 124; 32 rows at 128 (512K) 8 86, 4 90, and
+    // with 4 and 16 rows per softmax warp 88; at 256 (1M) 4 137 and 8 144 with peaked keys,
+    // 134 and 125 without; 48 rows (2 x 1M) 16 rows per softmax warp and 4 converting 674,
+    // 8 converting 907.
     static constexpr int HR = NR <= 32 ? 8 : 16;
-    static constexpr int ND = NR == 16 ? (D == 128 ? 16 : 8) : 4;
+    static constexpr int ND = NR == 16 ? (D == 128 ? 16 : 8) : NR == 32 && (D < 256 || LIVE == 24) ? 8 : 4;
     static constexpr int KG = ND == 16 ? 2 : 1, VG = KG;  // warp groups for K and V
     // Two groups take turns, each with slots of its own (a wait on a slot's barrier has to
     // follow every use of it).
@@ -951,7 +953,7 @@ template <int D>
 cudaError_t launch_kvq_attn_d(const KvqAttnParams &p, int n_cta, cudaStream_t stream) {
     // Rows past the last query's have no softmax warps where that frees a group of them: single
     // tokens of 16 sequences of 32K-64K, 8 rows of 128, 82 us (with warps for 16 rows 94); one
-    // sequence of 512K, 24 rows of 128, 82 (with warps for 32 rows 90).
+    // sequence of 512K, 24 rows of 128, 77 (with warps for 32 rows 86).
     if (p.rows <= 8) return launch_kvq_attn_nr<D, 16, 8>(p, n_cta, stream);
     switch ((p.rows + 15) / 16) {
         case 1: return launch_kvq_attn_nr<D, 16>(p, n_cta, stream);
