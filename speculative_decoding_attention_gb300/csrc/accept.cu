@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(kAcceptThreads, kAcceptPerSm) spec_accept_kern
                 if (ok) {
                     const float pv = __saturatef(P.target_probs[((int64_t)b * (P.k + 1) + j) * V + x]);
                     const float qv = P.draft_probs ? __saturatef(P.draft_probs[((int64_t)b * P.k + j) * V + x]) : 1.f;
-                    const float h = u * qv;
-                    ok = h < pv || (h == pv && fmaf(u, qv, -h) < 0.f);  // u q < p exactly
+                    // u q < p exactly: scaled so that the product's error cannot underflow where it matters
+                    const float us = u * 0x1p60f, qs = qv * 0x1p60f, ps = pv * 0x1p120f, h = us * qs;
+                    ok = h < ps || (h == ps && fmaf(us, qs, -h) < 0.f);
                 }
             }
             const unsigned bad = __ballot_sync(0xffffffffu, !ok);

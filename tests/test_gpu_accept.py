@@ -64,6 +64,29 @@ def test_ragged_drafts(noise):
         assert acc.cpu().tolist() == n.tolist()  # p = q: every draft is accepted
 
 
+@pytest.mark.parametrize("b", [60, 77, 153, 305, 700])
+@pytest.mark.parametrize("probs", [True, False])
+def test_batches_of_every_cluster_size(b, probs):
+    """8 CTAs per sequence down to one, and more sequences than are resident at once."""
+    gen = torch.Generator().manual_seed(b)
+    p, q, x, u, w = make(b, 2, 1301, gen)
+    check(p, q if probs else None, x, u, w)
+
+
+def test_smallest_probabilities_are_compared_exactly():
+    gen = torch.Generator().manual_seed(5)
+    b = 512
+    tiny = lambda lo, hi: torch.randint(lo, hi, (b,), generator=gen).double() * 2.0 ** -149  # noqa: E731
+    p, q = torch.zeros((b, 2, 3)), torch.zeros((b, 1, 3))
+    p[:, 0, 0], q[:, 0, 0] = tiny(0, 6).float(), tiny(1, 9).float()
+    p[:, 0, 1], p[:, 1, 2], q[:, 0, 1] = 1.0, 1.0, 1.0
+    u = torch.randint(0, 1 << 24, (b, 1), generator=gen).float() * 2.0 ** -24
+    u[::4] = 0.5 + 2.0 ** -24
+    u[1::4] = 0.5
+    u[2::4] = 0.5 - 2.0 ** -25
+    check(p, q, torch.zeros((b, 1), dtype=torch.int32), u, torch.rand((b,), generator=gen))
+
+
 def test_more_drafts_than_a_warp():
     gen = torch.Generator().manual_seed(2)
     p, q, x, u, w = make(5, 70, 300, gen, noise=0.0)
