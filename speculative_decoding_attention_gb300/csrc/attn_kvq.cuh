@@ -44,7 +44,7 @@
 //   NSW warps   softmax: a thread per lane (two keys of the tile), HR rows each; the four
 //               warps that share rows vote per tile whether the maxima have to be raised
 // What bounds it: HBM, as long as the instructions per tile fit beside it.  8 ragged paged
-// sequences, 12 rows of 128: 456 to 515 us, 4.7 to 5.3 TB/s; 1M positions, 32 rows of 256:
+// sequences, 12 rows of 128, 2.7 GB: 488 us, 5.5 TB/s; 1M positions, 32 rows of 256:
 // 137 us, 4.0; 2 x 1M positions, 40 rows of 128: 674 us, 3.4 -- there 54% of the issue slots
 // and 46% of the ALU are taken, the tensor pipe 35% (with the products of -8), and
 // registers bar more softmax warps.
@@ -75,7 +75,7 @@ struct KvqCfg {
     static constexpr int KU = D == 64 ? 2 : 4;          // 16-byte units per key and chunk
     // Rows per softmax warp and converting warps.  More warps hide more latency, fewer leave
     // more registers to each and repeat less per-key work; measured in us, chosen form first:
-    // up to 16 rows at head_dim 128 (ragged batch of 2.4 GB) 16 converting warps 515, 8 563, 4
+    // up to 16 rows at head_dim 128 (ragged batch of 2.9 GB) 16 converting warps 515, 8 563, 4
     // 644; at 64 (64 short sequences) 8 warps 54, 4 55, 16 61; 24 rows at 128 (512K positions)
     // 8 warps 77, 4 82; at 256 (1M) 8 115, 4 124; 32 rows at 128 (512K) 8 86, 4 90, and
     // with 4 and 16 rows per softmax warp 88; at 256 (1M) 4 137 and 8 144 with peaked keys,
