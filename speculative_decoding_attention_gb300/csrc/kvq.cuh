@@ -250,7 +250,7 @@ struct KvqWalk {
 cudaError_t launch_kvq_attn_d64(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_attn_d128(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 cudaError_t launch_kvq_attn_d256(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
-cudaError_t launch_kvq_merge(const KvqAttnParams &p, cudaStream_t stream);
+cudaError_t launch_kvq_merge(const KvqAttnParams &p, int n_cta, cudaStream_t stream);
 
 cudaError_t launch_kvq_append(const KvqView &c, const void *k_new, const void *v_new, int n_new, int32_t *err,
                               cudaStream_t stream);

@@ -890,7 +890,7 @@ wm_status wm_verify_attn_kvq(const wm_kvq *kv, const void *q, int32_t n_q, int32
                           : kv->head_dim == 128 ? launch_kvq_attn_d128(p, n_cta, st)
                                                 : launch_kvq_attn_d256(p, n_cta, st);
     if (e != cudaSuccess) return WM_ERR_CUDA;
-    return launch_status(launch_kvq_merge(p, st));
+    return launch_status(launch_kvq_merge(p, n_cta, st));
 }
 
 wm_status wm_spec_accept(const float *target_probs, const float *draft_probs, const int32_t *draft_tokens,
